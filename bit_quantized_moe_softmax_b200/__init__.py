@@ -22,6 +22,8 @@ _lib = None
 
 DS4MOE_ACT_F32 = 0
 DS4MOE_ACT_BF16 = 1
+DS4MOE_Q8_E4M3 = 0
+DS4MOE_Q8_INT8 = 1
 
 STATUS = {0: "OK", -1: "ERR_ARG", -2: "ERR_ALIGN", -3: "ERR_SHAPE", -4: "ERR_NOT_READY", -5: "ERR_CUDA",
           -6: "ERR_TIMEOUT", -7: "ERR_DEVICE"}
@@ -35,7 +37,8 @@ EXPORTS = ("ds4moe_create", "ds4moe_destroy", "ds4moe_weight_bytes", "ds4moe_wor
            "ds4moe_forward_residual_profiled", "ds4moe_set_steering", "ds4moe_forward_host_async",
            "ds4moe_host_sync", "ds4moe_probe", "ds4moe_selftest_wait",
            "ds4moe_permutation", "ds4moe_pack_q4k", "ds4moe_forward_chain", "ds4moe_forward_routed",
-           "ds4moe_combine_slots")
+           "ds4moe_combine_slots", "ds4moe_add_rmsnorm", "ds4moe_widen_rows", "ds4moe_project",
+           "ds4moe_project_work_bytes", "ds4moe_get_project_error", "ds4moe_sample")
 
 
 class ds4moe_shape(ctypes.Structure):
@@ -93,6 +96,13 @@ def lib() -> ctypes.CDLL:
             "ds4moe_combine_slots": ([vp, vp, vp, i32, i32, i32, vp, vp], i32),
             "ds4moe_set_steering": ([vp, vp, ctypes.c_float, vp], i32),
             "ds4moe_forward_residual_profiled": ([vp, vp, i32, vp, ctypes.POINTER(vp), vp], i32),
+            "ds4moe_add_rmsnorm": ([vp, i32, vp, i32, vp, ctypes.c_float, i32, i32, vp, vp, i32, vp, i32, i32, vp,
+                                    vp], i32),
+            "ds4moe_widen_rows": ([vp, i32, vp, i32, i32, i32, vp, i32, vp], i32),
+            "ds4moe_project": ([vp, i32, vp, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp], i32),
+            "ds4moe_project_work_bytes": ([i32, i32, i32, i32], sz),
+            "ds4moe_get_project_error": ([vp, ctypes.POINTER(i32)], i32),
+            "ds4moe_sample": ([vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -291,6 +301,158 @@ def ds4moe_get_device_error(h: int, stream=None) -> int:
     if st not in (0, -6, -7):
         _ok(st, "ds4moe_get_device_error")
     return code.value
+
+
+# ------------------------------------------------------------------ around the layer
+_ACT = {torch.float32: DS4MOE_ACT_F32, torch.bfloat16: DS4MOE_ACT_BF16}
+_Q8 = {torch.float8_e4m3fn: DS4MOE_Q8_E4M3, torch.int8: DS4MOE_Q8_INT8}
+
+
+def _refuse(where: str, msg: str):
+    raise Ds4MoeError(-1, where, msg)
+
+
+def _tensors(where: str, dev: torch.device, specs):
+    """Each (name, tensor or None, shape, dtypes): on dev, contiguous, of that shape and one of those types."""
+    for name, t, shape, dtypes in specs:
+        if t is None:
+            continue
+        if t.dtype not in dtypes:
+            _refuse(where, "%s: unsupported type %s" % (name, t.dtype))
+        if tuple(t.shape) != shape:
+            _refuse(where, "%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+        if t.device != dev or dev.type != "cuda":
+            _refuse(where, "%s: on %s, expected one CUDA device for all" % (name, t.device))
+        if not t.is_contiguous():
+            _refuse(where, "%s: not contiguous" % name)
+
+
+def _call(where: str, dev: torch.device, stream, fn, *args):
+    """fn(*args, stream) with dev current; the default stream is dev's current one."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _ok(fn(*args, _stream(stream)), where)
+    _ok(fn(*args, _stream(stream)), where)
+
+
+def _q8_groups(where: str, group: int, hidden: int) -> int:
+    if group not in (0, 32, 64, 128):
+        _refuse(where, "group %r (0, 32, 64 or 128)" % (group,))
+    return -(-hidden // group) if group else 1
+
+
+def ds4moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
+                       sum: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       q: torch.Tensor | None = None, scale: torch.Tensor | None = None, group: int = 128,
+                       stream=None):
+    """s = x + residual into ``sum``, its RMS norm times ``weight`` into ``out`` and, as 8-bit codes with one scale
+    per ``group`` columns (0: per row), into ``q`` (float8_e4m3fn or int8) and ``scale`` [n, groups].
+
+    x [n, H] and residual binary32 or bf16; ``sum`` of residual's type (it may be residual itself), ``out`` binary32
+    or bf16.  Outputs that are None are not written; at least one is needed.
+    """
+    where = "ds4moe_add_rmsnorm"
+    if x.dim() != 2:
+        _refuse(where, "x: %d dimensions, expected [n, hidden]" % x.dim())
+    n, H = x.shape
+    both = (torch.float32, torch.bfloat16)
+    shape = (n, H)
+    _tensors(where, x.device, (
+        ("x", x, shape, both), ("weight", weight, (H,), (torch.float32,)), ("residual", residual, shape, both),
+        ("sum", sum, shape, both if residual is None else (residual.dtype,)), ("out", out, shape, both),
+        ("q", q, shape, tuple(_Q8)),
+        ("scale", scale, (n, _q8_groups(where, group, H)), (torch.float32,))))
+    _call(where, x.device, stream, lib().ds4moe_add_rmsnorm, x.data_ptr(), _ACT[x.dtype], _ptr(residual),
+          0 if residual is None else _ACT[residual.dtype], weight.data_ptr(), eps, n, H, _ptr(sum), _ptr(out),
+          0 if out is None else _ACT[out.dtype], _ptr(q), 0 if q is None else _Q8[q.dtype], group, _ptr(scale))
+
+
+def ds4moe_widen_rows(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, group: int = 128, stream=None):
+    """out = q * scale: 8-bit rows of ds4moe_add_rmsnorm (codes [n, H], scales [n, groups]) as binary32 or bf16."""
+    where = "ds4moe_widen_rows"
+    if q.dim() != 2:
+        _refuse(where, "q: %d dimensions, expected [n, hidden]" % q.dim())
+    n, H = q.shape
+    _tensors(where, q.device, (("q", q, (n, H), tuple(_Q8)),
+                               ("scale", scale, (n, _q8_groups(where, group, H)), (torch.float32,)),
+                               ("out", out, (n, H), (torch.float32, torch.bfloat16))))
+    _call(where, q.device, stream, lib().ds4moe_widen_rows, q.data_ptr(), _Q8[q.dtype], scale.data_ptr(), group, n, H,
+          out.data_ptr(), _ACT[out.dtype])
+
+
+def ds4moe_project_work_bytes(n: int, out_features: int, n_adapters: int, rank: int) -> int:
+    return lib().ds4moe_project_work_bytes(n, out_features, n_adapters, rank)
+
+
+def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch.Tensor | None = None,
+                   B: torch.Tensor | None = None, adapter_scale: torch.Tensor | None = None,
+                   ids: torch.Tensor | None = None, work: torch.Tensor | None = None, stream=None):
+    """out = x W^T, plus adapter_scale[a] B[a] (A[a] x_i) for each row i whose adapter is a = ids[i].
+
+    bf16 x [n, in], W [out, in], A [adapters, rank, in], B [adapters, out, rank], out [n, out]; binary32
+    adapter_scale [adapters]; int32 ids [n], -1 for none.  ``work``: uint8 scratch of ds4moe_project_work_bytes
+    (allocated here by default).
+    """
+    where = "ds4moe_project"
+    if x.dim() != 2 or W.dim() != 2:
+        _refuse(where, "x: expected [n, in], W: [out, in]")
+    n, fin = x.shape
+    fout = W.shape[0]
+    bf = (torch.bfloat16,)
+    na = rank = wb = 0
+    if A is not None:
+        if B is None or adapter_scale is None or ids is None or A.dim() != 3:
+            _refuse(where, "adapters need A [adapters, rank, in], B, adapter_scale and ids")
+        na, rank = A.shape[0], A.shape[1]
+    elif B is not None or adapter_scale is not None or ids is not None:
+        _refuse(where, "B, adapter_scale and ids need A")
+    _tensors(where, x.device, (("x", x, (n, fin), bf), ("W", W, (fout, fin), bf), ("out", out, (n, fout), bf),
+                               ("A", A, (na, rank, fin), bf), ("B", B, (na, fout, rank), bf),
+                               ("adapter_scale", adapter_scale, (na,), (torch.float32,)),
+                               ("ids", ids, (n,), (torch.int32,))))
+    if na and n:
+        if work is None:
+            work = torch.empty(lib().ds4moe_project_work_bytes(n, fout, na, rank), dtype=torch.uint8, device=x.device)
+        elif work.device != x.device or not work.is_contiguous():
+            _refuse(where, "work: contiguous on %s expected" % x.device)
+        wb = work.numel() * work.element_size()
+    _call(where, x.device, stream, lib().ds4moe_project, x.data_ptr(), n, W.data_ptr(), fin, fout, _ptr(A), _ptr(B),
+          _ptr(adapter_scale), na, rank, _ptr(ids), out.data_ptr(), _ptr(work), wb)
+
+
+def ds4moe_get_project_error(stream=None) -> int:
+    code = ctypes.c_int32(0)
+    st = lib().ds4moe_get_project_error(_stream(stream), ctypes.byref(code))
+    if st not in (0, -6):
+        _ok(st, "ds4moe_get_project_error")
+    return code.value
+
+
+def ds4moe_sample(logits: torch.Tensor, u: torch.Tensor, token: torch.Tensor, temperature: torch.Tensor | None = None,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                  min_p: torch.Tensor | None = None, prob: torch.Tensor | None = None,
+                  probs: torch.Tensor | None = None, stream=None):
+    """The next token of each row of logits [n, vocab] (binary32 or bf16; rows may be strided) by the uniform
+    numbers u [n], after temperature, top-k, top-p and min-p (one value per row each, None: off).
+
+    token [n] int32; prob [n]: the token's probability; probs [n, vocab]: the filtered distribution.
+    """
+    where = "ds4moe_sample"
+    if logits.dim() != 2:
+        _refuse(where, "logits: %d dimensions, expected [n, vocab]" % logits.dim())
+    n, V = logits.shape
+    if logits.dtype not in _ACT:
+        _refuse(where, "logits: unsupported type %s" % logits.dtype)
+    if V > 1 and logits.stride(1) != 1:
+        _refuse(where, "logits: a row's elements must be next to each other")
+    f, one = (torch.float32,), (n,)
+    _tensors(where, logits.device, (("u", u, one, f), ("token", token, one, (torch.int32,)),
+                                    ("temperature", temperature, one, f), ("top_k", top_k, one, (torch.int32,)),
+                                    ("top_p", top_p, one, f), ("min_p", min_p, one, f), ("prob", prob, one, f),
+                                    ("probs", probs, (n, V), f)))
+    _call(where, logits.device, stream, lib().ds4moe_sample, logits.data_ptr(), _ACT[logits.dtype],
+          logits.stride(0) if n > 1 else V, n, V, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+          u.data_ptr(), token.data_ptr(), _ptr(prob), _ptr(probs))
 
 
 # ------------------------------------------------------------------ plumbing

@@ -106,6 +106,11 @@ struct WsLayout {
 
 }  // namespace
 
+// The status with its message, for the entry points of the other source files.
+namespace ds4 {
+ds4moe_status report(ds4moe_status s, const char* msg) { return fail(s, "%s", msg); }
+}  // namespace ds4
+
 struct ds4moe {
     ds4moe_shape shape;
     Dims D;

@@ -63,6 +63,9 @@ typedef enum {
 
 enum { DS4MOE_ACT_F32 = 0, DS4MOE_ACT_BF16 = 1 };
 
+/* 8-bit row formats: e4m3 codes (largest value 448) or int8 (-127 .. 127) */
+enum { DS4MOE_Q8_E4M3 = 0, DS4MOE_Q8_INT8 = 1 };
+
 typedef struct {
     int32_t hidden;        /* H: multiple of 256 */
     int32_t inter;         /* I: multiple of 256, or 128 */
@@ -213,6 +216,95 @@ ds4moe_status ds4moe_forward_routed(ds4moe_t* h, const void* d_x, int32_t n_toke
  * or NULL (zero), d_out [n][H]: device binary32; d_out may alias d_base. */
 ds4moe_status ds4moe_combine_slots(const float* d_y, const float* d_w, const float* d_base, int32_t n, int32_t k,
                                    int32_t hidden, float* d_out, void* stream);
+
+/* ---- around the layer (no handle) ----------------------------------------
+ * The steps between layers and after the last one.  Element types are
+ * DS4MOE_ACT_F32 / DS4MOE_ACT_BF16; tensors are contiguous unless a function
+ * takes a stride; an output that overlaps another buffer of the call is
+ * DS4MOE_ERR_ARG; n == 0 is a no-op.  Launches only (on the current device,
+ * which must be the buffers'), safe to capture in a CUDA graph. */
+
+/* Residual addition and root-mean-square norm, the step in front of a layer:
+ *   s = x + residual     one binary32 add, rounded to the residual's type
+ *                        (without a residual s = x)
+ *   y = (s rstd) w       rstd = 1 / sqrt(mean(s^2) + eps), two binary32 products
+ * with the mean in binary64 and rstd rounded to binary32 once, so that the
+ * results, the 8-bit codes included, do not depend on the split of the work.
+ * d_x [n][hidden], d_residual [n][hidden] or NULL, d_weight [hidden] binary32.
+ * Outputs, each or NULL but not all: d_sum = s in the residual's type (may be
+ * d_residual itself: the stream is updated in place); d_out = y; d_q = y as
+ * 8-bit codes of q_format with d_scale [n][ceil(hidden / group)] binary32
+ * (group 32, 64 or 128 columns; group 0: one scale per row, [n]): scale =
+ * max|y| of the group / 448 (e4m3) or / 127 (int8), code = y / scale rounded
+ * to nearest even; a group of zeros has scale 0 and codes 0, a group with a
+ * value that is not finite widens to NaN.  hidden <= 16384 (DS4MOE_ERR_SHAPE);
+ * eps positive and finite; d_x, d_residual, d_weight, d_sum, d_out and d_q
+ * 16-byte aligned. */
+ds4moe_status ds4moe_add_rmsnorm(const void* d_x, int32_t x_dtype, const void* d_residual, int32_t residual_dtype,
+                                 const float* d_weight, float eps, int32_t n, int32_t hidden, void* d_sum, void* d_out,
+                                 int32_t out_dtype, void* d_q, int32_t q_format, int32_t group, float* d_scale,
+                                 void* stream);
+
+/* Rows of 8-bit codes back to values: out = code * scale, one binary32 product
+ * (rounded once more where out is bf16).  Layouts as ds4moe_add_rmsnorm's d_q
+ * and d_scale; d_q and d_out 16-byte aligned.  What a rank that received 8-bit
+ * rows calls before its experts. */
+ds4moe_status ds4moe_widen_rows(const void* d_q, int32_t q_format, const float* d_scale, int32_t group, int32_t n,
+                                int32_t hidden, void* d_out, int32_t out_dtype, void* stream);
+
+/* A shared projection with low-rank adapters of many requests beside it:
+ *   out_i = W x_i + scale_a B_a (A_a x_i),  a = d_ids[i]
+ * all bf16 with binary32 accumulation and one rounding of the sum; A_a x_i
+ * enters the second product with 16 bits.  d_x [n][in], d_W [out][in], d_A
+ * [n_adapters][rank][in], d_B [n_adapters][out][rank], d_scale [n_adapters]
+ * binary32, d_ids [n] int32: an id outside 0 .. n_adapters-1 (-1, say) means
+ * no adapter.  n_adapters 0: the projection alone (the adapter arguments and
+ * the work buffer are ignored).  Rows may come in any order; rows of one
+ * adapter next to each other are fastest (the cost of the adapters goes by the
+ * distinct ones among a tile's rows).  in a multiple of 8 up to 65536, out
+ * <= 2^20, rank a multiple of 8 in 8 .. 128, n_adapters <= 65536
+ * (DS4MOE_ERR_SHAPE), n <= 2^20; x, W, A, B, out 16-byte aligned.  d_work: device scratch of at least
+ * ds4moe_project_work_bytes bytes, 256-byte aligned, this call's alone until
+ * it has run.  A bounded device-side wait that gives up leaves NaN in out and
+ * sets the word that ds4moe_get_project_error reads. */
+ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_t in_features, int32_t out_features,
+                             const void* d_A, const void* d_B, const float* d_scale, int32_t n_adapters, int32_t rank,
+                             const int32_t* d_ids, void* d_out, void* d_work, size_t work_bytes, void* stream);
+
+/* Bytes of scratch a ds4moe_project of n rows needs (0 without adapters, and
+ * for sizes that it refuses): about n * min(256, n_adapters) * rank * 4. */
+size_t ds4moe_project_work_bytes(int32_t n, int32_t out_features, int32_t n_adapters, int32_t rank);
+
+/* Synchronize `stream`, then read and clear the current device's error word of
+ * ds4moe_project into *code (0 = none, bit 1 = a bounded wait timed out, with
+ * DS4MOE_ERR_TIMEOUT). */
+ds4moe_status ds4moe_get_project_error(void* stream, int32_t* code);
+
+/* The next token of each row of logits (n rows of `vocab` elements of `dtype`,
+ * row_stride elements apart), by a given uniform number: with M the row's
+ * largest logit and w_i = exp((l_i - M) / T), the tokens ordered by (logit
+ * descending, index ascending),
+ *   top-k keeps the first k; top-p the shortest prefix whose w sum to at least
+ *   p of the top-k set's; min-p the tokens with w >= min_p (w = 1 for M);
+ * token = the first kept one, in index order, whose running sum of w exceeds u
+ * times the kept total.  d_temperature, d_top_k, d_top_p, d_min_p: one value
+ * per row, or NULL for off.  T <= 0 (or NaN) is greedy: the first token of the
+ * order, whatever the filters and u; off are top_k < 1 or >= vocab, top_p >= 1
+ * or NaN, min_p <= 0 or NaN; at least the first token is kept.  d_u [n] in
+ * [0, 1); a value below (or NaN) counts as 0, one above draws the last kept
+ * token.  A NaN logit counts as -infinity; tokens at -infinity are never drawn,
+ * and a row of nothing else gives token -1.  Logits at +infinity share all the
+ * weight.
+ * Outputs: d_token [n] int32; d_prob [n] binary32 or NULL: the token's share
+ * of the kept total; d_probs [n][vocab] binary32 or NULL: every token's share,
+ * 0 where removed (what the verification of drafted tokens reads).  Weights are
+ * summed as integers in units of 2^-44 (those that round to 0 are never
+ * drawn), so results do not depend on the order of work.  vocab <= 262144
+ * (DS4MOE_ERR_SHAPE). */
+ds4moe_status ds4moe_sample(const void* d_logits, int32_t dtype, int64_t row_stride, int32_t n, int32_t vocab,
+                            const float* d_temperature, const int32_t* d_top_k, const float* d_top_p,
+                            const float* d_min_p, const float* d_u, int32_t* d_token, float* d_prob, float* d_probs,
+                            void* stream);
 
 /* A chain of layers on the decode plan: x_{l+1} = x_l + layer_l(x_l) for
  * l = 0 .. n_layers-1 (layers[l] applied to the previous layer's output),
