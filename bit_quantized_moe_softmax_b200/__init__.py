@@ -312,27 +312,36 @@ def _refuse(where: str, msg: str):
     raise Ds4MoeError(-1, where, msg)
 
 
-def _tensors(where: str, dev: torch.device, specs):
-    """Each (name, tensor or None, shape, dtypes): on dev, contiguous, of that shape and one of those types."""
-    for name, t, shape, dtypes in specs:
-        if t is None:
+def _tensors(where: str, dev: int, specs):
+    """Each (name, tensor or None, shape, types): on CUDA device dev, contiguous, of that shape and one of the types."""
+    for name, t, shape, types in specs:
+        if t is None or (t.dtype in types and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+                         and dev >= 0):
             continue
-        if t.dtype not in dtypes:
+        if t.dtype not in types:
             _refuse(where, "%s: unsupported type %s" % (name, t.dtype))
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             _refuse(where, "%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
-        if t.device != dev or dev.type != "cuda":
+        if dev < 0 or t.get_device() != dev:
             _refuse(where, "%s: on %s, expected one CUDA device for all" % (name, t.device))
-        if not t.is_contiguous():
-            _refuse(where, "%s: not contiguous" % name)
+        _refuse(where, "%s: not contiguous" % name)
 
 
-def _call(where: str, dev: torch.device, stream, fn, *args):
-    """fn(*args, stream) with dev current; the default stream is dev's current one."""
-    if dev.index != torch.cuda.current_device():
+def _call(where: str, dev: int, stream, fn, *args):
+    """fn(*args, stream) with device dev current; the default stream is dev's current one."""
+    if dev < 0:
+        _refuse(where, "expected CUDA tensors")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = _stream(stream)
+    if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            return _ok(fn(*args, _stream(stream)), where)
-    _ok(fn(*args, _stream(stream)), where)
+            status = fn(*args, stream)
+    else:
+        status = fn(*args, stream)
+    if status:
+        _ok(status, where)
 
 
 def _q8_groups(where: str, group: int, hidden: int) -> int:
@@ -355,14 +364,14 @@ def ds4moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residu
     if x.dim() != 2:
         _refuse(where, "x: %d dimensions, expected [n, hidden]" % x.dim())
     n, H = x.shape
-    both = (torch.float32, torch.bfloat16)
+    dev = x.get_device()
     shape = (n, H)
-    _tensors(where, x.device, (
-        ("x", x, shape, both), ("weight", weight, (H,), (torch.float32,)), ("residual", residual, shape, both),
-        ("sum", sum, shape, both if residual is None else (residual.dtype,)), ("out", out, shape, both),
-        ("q", q, shape, tuple(_Q8)),
+    _tensors(where, dev, (
+        ("x", x, shape, _ACT), ("weight", weight, (H,), (torch.float32,)), ("residual", residual, shape, _ACT),
+        ("sum", sum, shape, _ACT if residual is None else (residual.dtype,)), ("out", out, shape, _ACT),
+        ("q", q, shape, _Q8),
         ("scale", scale, (n, _q8_groups(where, group, H)), (torch.float32,))))
-    _call(where, x.device, stream, lib().ds4moe_add_rmsnorm, x.data_ptr(), _ACT[x.dtype], _ptr(residual),
+    _call(where, dev, stream, lib().ds4moe_add_rmsnorm, x.data_ptr(), _ACT[x.dtype], _ptr(residual),
           0 if residual is None else _ACT[residual.dtype], weight.data_ptr(), eps, n, H, _ptr(sum), _ptr(out),
           0 if out is None else _ACT[out.dtype], _ptr(q), 0 if q is None else _Q8[q.dtype], group, _ptr(scale))
 
@@ -373,10 +382,11 @@ def ds4moe_widen_rows(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, g
     if q.dim() != 2:
         _refuse(where, "q: %d dimensions, expected [n, hidden]" % q.dim())
     n, H = q.shape
-    _tensors(where, q.device, (("q", q, (n, H), tuple(_Q8)),
+    dev = q.get_device()
+    _tensors(where, dev, (("q", q, (n, H), _Q8),
                                ("scale", scale, (n, _q8_groups(where, group, H)), (torch.float32,)),
-                               ("out", out, (n, H), (torch.float32, torch.bfloat16))))
-    _call(where, q.device, stream, lib().ds4moe_widen_rows, q.data_ptr(), _Q8[q.dtype], scale.data_ptr(), group, n, H,
+                               ("out", out, (n, H), _ACT)))
+    _call(where, dev, stream, lib().ds4moe_widen_rows, q.data_ptr(), _Q8[q.dtype], scale.data_ptr(), group, n, H,
           out.data_ptr(), _ACT[out.dtype])
 
 
@@ -397,6 +407,7 @@ def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch
     if x.dim() != 2 or W.dim() != 2:
         _refuse(where, "x: expected [n, in], W: [out, in]")
     n, fin = x.shape
+    dev = x.get_device()
     fout = W.shape[0]
     bf = (torch.bfloat16,)
     na = rank = wb = 0
@@ -406,17 +417,17 @@ def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch
         na, rank = A.shape[0], A.shape[1]
     elif B is not None or adapter_scale is not None or ids is not None:
         _refuse(where, "B, adapter_scale and ids need A")
-    _tensors(where, x.device, (("x", x, (n, fin), bf), ("W", W, (fout, fin), bf), ("out", out, (n, fout), bf),
+    _tensors(where, dev, (("x", x, (n, fin), bf), ("W", W, (fout, fin), bf), ("out", out, (n, fout), bf),
                                ("A", A, (na, rank, fin), bf), ("B", B, (na, fout, rank), bf),
                                ("adapter_scale", adapter_scale, (na,), (torch.float32,)),
                                ("ids", ids, (n,), (torch.int32,))))
     if na and n:
         if work is None:
             work = torch.empty(lib().ds4moe_project_work_bytes(n, fout, na, rank), dtype=torch.uint8, device=x.device)
-        elif work.device != x.device or not work.is_contiguous():
+        elif work.get_device() != dev or not work.is_contiguous():
             _refuse(where, "work: contiguous on %s expected" % x.device)
         wb = work.numel() * work.element_size()
-    _call(where, x.device, stream, lib().ds4moe_project, x.data_ptr(), n, W.data_ptr(), fin, fout, _ptr(A), _ptr(B),
+    _call(where, dev, stream, lib().ds4moe_project, x.data_ptr(), n, W.data_ptr(), fin, fout, _ptr(A), _ptr(B),
           _ptr(adapter_scale), na, rank, _ptr(ids), out.data_ptr(), _ptr(work), wb)
 
 
@@ -441,16 +452,17 @@ def ds4moe_sample(logits: torch.Tensor, u: torch.Tensor, token: torch.Tensor, te
     if logits.dim() != 2:
         _refuse(where, "logits: %d dimensions, expected [n, vocab]" % logits.dim())
     n, V = logits.shape
+    dev = logits.get_device()
     if logits.dtype not in _ACT:
         _refuse(where, "logits: unsupported type %s" % logits.dtype)
     if V > 1 and logits.stride(1) != 1:
         _refuse(where, "logits: a row's elements must be next to each other")
     f, one = (torch.float32,), (n,)
-    _tensors(where, logits.device, (("u", u, one, f), ("token", token, one, (torch.int32,)),
+    _tensors(where, dev, (("u", u, one, f), ("token", token, one, (torch.int32,)),
                                     ("temperature", temperature, one, f), ("top_k", top_k, one, (torch.int32,)),
                                     ("top_p", top_p, one, f), ("min_p", min_p, one, f), ("prob", prob, one, f),
                                     ("probs", probs, (n, V), f)))
-    _call(where, logits.device, stream, lib().ds4moe_sample, logits.data_ptr(), _ACT[logits.dtype],
+    _call(where, dev, stream, lib().ds4moe_sample, logits.data_ptr(), _ACT[logits.dtype],
           logits.stride(0) if n > 1 else V, n, V, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
           u.data_ptr(), token.data_ptr(), _ptr(prob), _ptr(probs))
 

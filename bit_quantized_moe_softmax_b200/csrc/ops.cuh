@@ -47,7 +47,7 @@ struct SampleArgs {
     int32_t* token;       // [n]
     float* prob;          // [n] or nullptr
     float* probs;         // [n][V] or nullptr
-    int slice;            // tokens per CTA, set by the launcher
+    int slice, seg;       // tokens per CTA and per warp, set by the launcher
 };
 cudaError_t launch_sample(SampleArgs a, bool bf16, int n, cudaStream_t st);
 

@@ -2,10 +2,9 @@
 // and min-p, then one draw by a given uniform number.
 //
 // With M the row's largest logit and w_i = exp((l_i - M) / T), all three
-// filters keep a prefix of the tokens ordered by (logit desc, index asc), so
-// the kept set is "key above a threshold, and the first q of the tokens at
-// it" (key: the logit's bits in an order-preserving form) and no sort is
-// needed.  The draw goes through the kept tokens by index: the first whose
+// filters keep a prefix of the tokens ordered by (logit desc, index asc): the
+// tokens above a logit, and those at it up to an index.  So no sort of the row
+// is needed.  The draw goes through the kept tokens by index: the first whose
 // running sum of weights exceeds u times their total.
 //
 // Weights are held as integers, round(w 2^44) (at most 2^18 tokens, so sums
@@ -17,8 +16,9 @@
 // as binary32 (up to 32,768 tokens each): one read of the logits from HBM,
 // every further pass is on chip, and sums meet through distributed shared
 // memory.  A filter's threshold is found by histograms of 2,048 bins: first
-// over (M - l) / T in steps of 1/64, then, inside the bin that holds the
-// prefix's end, over the keys' bits (at most three rounds, usually one or two).
+// over M - l in small steps; the tokens of the bin that holds the prefix's end
+// are then sorted, or, where there are more than 512 (logits of few bits have
+// many ties), counted over their keys' bits.
 #include <cooperative_groups.h>
 
 #include "ds4moe_internal.cuh"
@@ -35,22 +35,29 @@ constexpr int kSW = kST / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kList = kST;                  // tokens of one bin that are put in order at once
+constexpr int kTab = 128;                   // entries of the table of 2^(j / 128)
 constexpr double kOne = 17592186044416.0;   // 2^44
+constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: adding it leaves the nearest integer in the low bits
 constexpr float kNegInf = -INFINITY;
 
 typedef unsigned long long u64;
 
-struct SampleSmem {
-    u64 hist[kBins];
+struct __align__(16) SampleSmem {
+    uint32_t hist[2][2][kBins];      // two in turn: counts in the first array, or the low and high words of weights
+    u64 group[2][kMaxCluster][32];   // sums of 64 bins of each CTA, written by the peers; two in turn
+    u64 part[kMaxCluster][64];       // one group's bins of each CTA
+    u64 list[kList];                 // this CTA's tokens of a bin (the first kList / C), then all of them in order
+    uint32_t listed[kMaxCluster];    // how many there are in each CTA
+    uint32_t list_n;
+    double tab[kTab];
     u64 wsum[kSW];
     u64 slice_tot[kMaxCluster];      // written by the peers
-    u64 mass[kMaxCluster];
-    u64 found_before;
-    uint32_t found_bin;
     uint32_t wtie[kSW];
     float mx[kMaxCluster];
     uint32_t klo[kMaxCluster], khi[kMaxCluster];
     uint32_t ties[kMaxCluster];
+    int tie_at;
     float wmax[kSW];
     uint32_t wlo[kSW], whi[kSW];
 };
@@ -59,108 +66,175 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t u = __float_as_uint(v);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-// exp((l - M) / T) of one token in binary64; tokens at -infinity weigh nothing,
-// and where M is +infinity only the tokens there weigh (the limit).
+// exp((l - M) / T) of one token in binary64: 2^(y / 128), y = (l - M) 128
+// log2(e) / T, from a table of 2^(j / 128) and four terms of the series of
+// 2^(r / 128), |r| <= 1/2 (a little more, as binary32 finds the nearest
+// integer): the fifth is below 2e-15, a twentieth of the unit 2^-44.  Ten
+// binary64 operations; 16,384 tokens take 3,500 clocks of an SM (CUDA's own
+// exp: twice that).  Free of branches, so that several are in flight.  The
+// result is not used for l = -infinity.
 struct Weigh {
-    double M, inv;
-    bool top_inf;
+    double M, c;           // c = 128 log2(e) / T
+    float Mf, cf;
+    const double* tab;
     __device__ __forceinline__ double operator()(float l) const {
-        if (l == kNegInf) return 0.0;
-        if (top_inf) return l == INFINITY ? 1.0 : 0.0;
-        const double d = ((double)l - M) * inv;
-        return d < -31.2 ? 0.0 : exp(d);   // e^-31.2 is half a unit of 2^-44: rounds to zero
+        // the nearest integer by a binary32 addition (an F2I has an eighth of its rate); -8192 and NaN weigh nothing
+        const int k = __float_as_int(fmaxf((l - Mf) * cf, -8192.f) + 12582912.f) - 0x4b400000;
+        const double kd = __hiloint2double(0x43380000 + (k >> 31), k) - kMagic;
+        const double r = fma((double)l - M, c, -kd);
+        constexpr double h = 0.69314718055994530942 / kTab;
+        double p = fma(r, h * h * h * h / 24.0, h * h * h / 6.0);
+        p = fma(r, p, h * h / 2.0);
+        p = fma(r, p, h);
+        p *= r;
+        double w = tab[k & (kTab - 1)];
+        w = fma(w, p, w);
+        w = __hiloint2double(__double2hiint(w) + ((k >> 7) << 20), __double2loint(w));
+        return k < -46 * kTab ? 0.0 : w;   // below half a unit by far
     }
-    __device__ __forceinline__ u64 units(float l) const { return (u64)__double2ll_rn((*this)(l) * kOne); }
+    static __device__ __forceinline__ u64 to_units(double w) {
+        return (u64)(__double_as_longlong(fma(w, kOne, kMagic)) - __double_as_longlong(kMagic));
+    }
+    __device__ __forceinline__ u64 units(float l) const { return to_units((*this)(l)); }
 };
 
-// Bin of the first histogram: monotone in l, so any rounding is as good.
+// Bin of the first histogram: (M - l) in steps, the last bin for all beyond.
+// Monotone in l, so any rounding is as good.
 struct Coarse {
-    float M, finv;
-    bool top_inf;
+    float M, step;   // 1 / step length, between 1e-38 and 1e38: no product of 0 and infinity
     __device__ __forceinline__ uint32_t operator()(float l) const {
-        if (top_inf) return l == INFINITY ? 0u : (uint32_t)(kBins - 1);
-        return min((uint32_t)__float2int_rz((M - l) * finv), (uint32_t)(kBins - 1));   // NaN (0 * inf) gives 0
+        return __float_as_uint(fminf((M - l) * step, (float)(kBins - 1)) + 8388608.f) - 0x4b000000u;
     }
 };
 
-// The histogram's first bin at which the running sum over all CTAs of the
-// cluster reaches target, and the sum before it; false if the total is below.
-// Every CTA's hist must be complete (this starts with a cluster barrier).
-__device__ bool find_bin(cg::cluster_group& cl, SampleSmem& S, u64 target, uint32_t& bin, u64& before) {
-    const int C = (int)cl.num_blocks(), r = (int)cl.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = kBins / C;   // this CTA's share of the bins
-    const int each = (per + kST - 1) / kST;   // consecutive bins per thread
-    cl.sync();
-    u64 v[kBins / kST], sum = 0;
+__device__ __forceinline__ u64 warp_sum(u64 v) {
 #pragma unroll
-    for (int j = 0; j < kBins / kST; ++j) {
-        v[j] = 0;
-        const int b = tid * each + j;
-        if (j < each && b < per) {
-            for (int p = 0; p < C; ++p) v[j] += cl.map_shared_rank(S.hist, p)[r * per + b];
-        }
-        sum += v[j];
-    }
-    u64 inc = sum;   // inclusive scan over the CTA's threads
+    for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(kAll, v, m);
+    return v;
+}
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {   // inclusive
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const u64 o = __shfl_up_sync(kAll, inc, m);
-        if (lane >= m) inc += o;
+        const u64 o = __shfl_up_sync(kAll, v, m);
+        if (lane >= m) v += o;
     }
-    if (lane == 31) S.wsum[warp] = inc;
+    return v;
+}
+
+// Sums of 64 bins of this CTA's histogram `buf` to every CTA of the cluster.
+// The histogram must be complete; a cluster barrier follows before find_bin.
+template <int C>
+__device__ __forceinline__ void push_groups(cg::cluster_group& cl, SampleSmem& S, int buf, bool wide) {
+    static_assert(kBins == 4 * kST, "four bins per thread");
+    const int r = C == 1 ? 0 : (int)cl.block_rank(), tid = threadIdx.x;
+    const uint4 lo = reinterpret_cast<const uint4*>(S.hist[buf][0])[tid];
+    u64 v = (u64)lo.x + lo.y + lo.z + lo.w;
+    if (wide) {
+        const uint4 hi = reinterpret_cast<const uint4*>(S.hist[buf][1])[tid];
+        v += ((u64)hi.x + hi.y + hi.z + hi.w) << 32;
+    }
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) v += __shfl_xor_sync(kAll, v, m);
+    const int p = tid & 15;   // sixteen threads hold the sum
+    if (p < C) cl.map_shared_rank(&S.group[0][0][0], p)[(buf * kMaxCluster + r) * 32 + (tid >> 4)] = v;
+}
+
+// After the barrier: the sum of this histogram over the cluster.
+template <int C>
+__device__ __forceinline__ u64 group_scan(SampleSmem& S, int buf, int lane, u64& inc, u64& mine) {
+    mine = 0;
+#pragma unroll
+    for (int p = 0; p < C; ++p) mine += S.group[buf][p][lane];
+    inc = warp_scan(mine, lane);
+    return __shfl_sync(kAll, inc, 31);
+}
+
+// The histogram's first bin at which the running sum over the cluster reaches
+// target (1 .. its total), the sum before it and the bin's own.  Every CTA
+// reads the 64 bins of one group from its peers and finds the same answer.
+template <int C>
+__device__ __noinline__ void find_bin(SampleSmem& S, int buf, bool wide, u64 target, uint32_t& bin, u64& before,
+                                      u64& own) {
+    cg::cluster_group cl = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31;
+    u64 inc, mine;
+    group_scan<C>(S, buf, lane, inc, mine);
+    const int g = __ffs(__ballot_sync(kAll, inc >= target)) - 1;
+    before = __shfl_sync(kAll, inc - mine, g);
+    for (int i = tid; i < 64 * C; i += kST) {
+        const uint32_t* h = cl.map_shared_rank(&S.hist[0][0][0], i >> 6) + 2 * buf * kBins + g * 64 + (i & 63);
+        const uint32_t lo = h[0], hi = wide ? h[kBins] : 0u;
+        S.part[i >> 6][i & 63] = (u64)lo | ((u64)hi << 32);
+    }
     __syncthreads();
-    u64 base = 0, tot = 0;
+    u64 a = 0, b = 0;   // bins 2 lane, 2 lane + 1
 #pragma unroll
-    for (int w = 0; w < kSW; ++w) {
-        if (w < warp) base += S.wsum[w];
-        tot += S.wsum[w];
-    }
-    if (tid < C) cl.map_shared_rank(S.slice_tot, tid)[r] = tot;
-    cl.sync();
-    u64 all = 0;
     for (int p = 0; p < C; ++p) {
-        if (p < r) base += S.slice_tot[p];
-        all += S.slice_tot[p];
+        const ulonglong2 v = reinterpret_cast<const ulonglong2*>(S.part[p])[lane];
+        a += v.x, b += v.y;
     }
-    u64 cum = base + inc - sum;
-    if (all >= target) {
-#pragma unroll
-        for (int j = 0; j < kBins / kST; ++j) {
-            if (cum < target && cum + v[j] >= target) {   // one thread of the cluster
-                for (int p = 0; p < C; ++p) {
-                    SampleSmem* o = cl.map_shared_rank(&S, p);
-                    o->found_bin = (uint32_t)(r * per + tid * each + j);
-                    o->found_before = cum;
-                }
+    inc = warp_scan(a + b, lane);
+    const int at = __ffs(__ballot_sync(kAll, before + inc >= target)) - 1;
+    u64 pre = before + inc - a - b;
+    const bool second = pre + a < target;
+    if (second) pre += a;
+    bin = __shfl_sync(kAll, (uint32_t)(g * 64 + 2 * lane + second), at);
+    own = __shfl_sync(kAll, second ? b : a, at);
+    before = __shfl_sync(kAll, pre, at);
+    __syncthreads();   // S.part is free again
+}
+
+// A token in the order of the filters, largest first: key, then the lower index.
+__device__ __forceinline__ u64 order_of(uint32_t key, int idx) { return ((u64)key << 32) | (uint32_t)~idx; }
+
+// One value per thread of the CTA, sorted: thread 0 gets the largest (bitonic
+// network: steps inside a warp by shuffles, the others through shared memory).
+__device__ __noinline__ u64 sort_desc(SampleSmem& S, u64 v) {
+    const int tid = threadIdx.x;
+    for (int k = 2; k <= kST; k <<= 1) {
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            u64 o;
+            if (j >= 32) {
+                S.list[tid] = v;
+                __syncthreads();
+                o = S.list[tid ^ j];
+                __syncthreads();
+            } else {
+                o = __shfl_xor_sync(kAll, v, j);
             }
-            cum += v[j];
+            const bool larger = ((tid & j) == 0) == ((tid & k) == 0);   // this thread keeps the larger one
+            if (larger == (o > v)) v = o;
         }
     }
-    cl.sync();
-    bin = S.found_bin;
-    before = S.found_before;
-    return all >= target;
+    return v;
 }
 
 }  // namespace
 
-template <bool BF>
-__global__ void __launch_bounds__(kST) k_sample(SampleArgs a) {
-    extern __shared__ float vals[];   // [slice]
+template <bool BF, int C>
+__global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
+    extern __shared__ __align__(16) float vals[];   // [kSW][a.seg]: each warp's share of the CTA's tokens, in index order
     __shared__ SampleSmem S;
     cg::cluster_group cl = cg::this_cluster();
-    const int C = (int)cl.num_blocks(), r = (int)cl.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = C == 1 ? 0 : (int)cl.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / C;
     const int begin = r * a.slice;
     const int cnt = max(0, min(a.V - begin, a.slice));
 
+    // ---- this row's parameters
+    float T = a.temp ? a.temp[row] : 1.f;
+    int K = a.top_k ? a.top_k[row] : 0;
+    float P = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
+    if (!(T > 0.f)) T = 1.f, K = 1, P = 1.f, mp = 0.f, u = 0.f;   // greedy: the first token of the order
+
     // ---- the row into shared memory, and its maximum; a NaN counts as -infinity
     float mx = kNegInf;
-    auto take = [&](int i, float v) {
+    auto clean = [&](float v) {
         v = v == v ? v + 0.f : kNegInf;   // -0 and +0 tie
-        vals[i] = v;
         mx = fmaxf(mx, v);
+        return v;
     };
     {
         const char* src = static_cast<const char*>(a.logits) + (row * a.ld + begin) * (BF ? 2 : 4);
@@ -168,36 +242,47 @@ __global__ void __launch_bounds__(kST) k_sample(SampleArgs a) {
         if (((uintptr_t)src & 15) == 0) {
             constexpr int E = BF ? 8 : 4;
             const int nv = cnt / E;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = tid; i < nv; i += kST) {
                 const uint4 w = ld_stream_v4(src + (size_t)i * 16);
                 const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                float4* d = reinterpret_cast<float4*>(vals + i * E);
+                if constexpr (BF) {
+                    float f[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (BF) {
-                        take(i * 8 + 2 * j, __uint_as_float(x[j] << 16));
-                        take(i * 8 + 2 * j + 1, __uint_as_float(x[j] & 0xffff0000u));
-                    } else {
-                        take(i * 4 + j, __uint_as_float(x[j]));
+                    for (int j = 0; j < 4; ++j) {
+                        f[2 * j] = clean(__uint_as_float(x[j] << 16));
+                        f[2 * j + 1] = clean(__uint_as_float(x[j] & 0xffff0000u));
                     }
+                    d[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    d[1] = make_float4(f[4], f[5], f[6], f[7]);
+                } else {
+                    d[0] = make_float4(clean(__uint_as_float(x[0])), clean(__uint_as_float(x[1])),
+                                       clean(__uint_as_float(x[2])), clean(__uint_as_float(x[3])));
                 }
             }
             done = nv * E;
         }
-#pragma unroll 4
+#pragma unroll 8
         for (int i = done + tid; i < cnt; i += kST) {
-            if constexpr (BF) take(i, __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(src)[i] << 16));
-            else take(i, reinterpret_cast<const float*>(src)[i]);
+            if constexpr (BF) vals[i] = clean(__uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(src)[i] << 16));
+            else vals[i] = clean(reinterpret_cast<const float*>(src)[i]);
         }
+        for (int i = cnt + tid; i < kSW * a.seg; i += kST) vals[i] = kNegInf;
     }
+    if (tid < kTab) S.tab[tid] = exp2((double)tid / kTab);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, m));
     if (lane == 0) S.wmax[warp] = mx;
     __syncthreads();
+#pragma unroll
     for (int w = 0; w < kSW; ++w) mx = fmaxf(mx, S.wmax[w]);
-    if (tid < C) cl.map_shared_rank(S.mx, tid)[r] = mx;
-    cl.sync();
-    for (int p = 0; p < C; ++p) mx = fmaxf(mx, S.mx[p]);
+    if (C > 1) {
+        if (tid < C) cl.map_shared_rank(S.mx, tid)[r] = mx;
+        cl.sync();
+#pragma unroll
+        for (int p = 0; p < C; ++p) mx = fmaxf(mx, S.mx[p]);
+    }
 
     float* probs = a.probs ? a.probs + row * a.V + begin : nullptr;
     if (mx == kNegInf) {   // nothing to draw from
@@ -210,172 +295,309 @@ __global__ void __launch_bounds__(kST) k_sample(SampleArgs a) {
         return;
     }
 
-    // ---- this row's parameters
-    float T = a.temp ? a.temp[row] : 1.f;
-    int K = a.top_k ? a.top_k[row] : 0;
-    float P = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
-    if (!(T > 0.f)) T = 1.f, K = 1, P = 1.f, mp = 0.f, u = 0.f;   // greedy: the first token of the order
+    if (mx == INFINITY) {   // the tokens there share all the weight
+        for (int i = tid; i < kSW * a.seg; i += kST) vals[i] = vals[i] == INFINITY ? 0.f : kNegInf;
+        mx = 0.f;
+        __syncthreads();
+    }
     const bool by_k = K >= 1 && K < a.V, by_p = P < 1.f, by_m = mp > 0.f;
     const double minw = fmin((double)mp, 1.0);
-    const double inv = 1.0 / (double)T;
-    const Weigh weigh{(double)mx, inv, mx == INFINITY};
-    const Coarse coarse{mx, (float)(inv * 64.0), mx == INFINITY};
+    const double inv = 1.0 / (double)T, c = inv * (kTab * 1.44269504088896340736);
+    const Weigh weigh{(double)mx, c, mx, (float)fmin(c, 1e38), S.tab};
+    const int s0 = warp * a.seg;   // this warp's tokens: s0 .. s0 + seg - 1
 
-    // ---- the prefix that top-k and top-p keep: keys above kt, and q of those at kt
-    uint32_t kt = 0;
-    u64 q = ~0ull;
+    // ---- the prefix that top-k and top-p keep: tokens above thr, and those at it up to index last of the row
+    float thr = -3.402823466e38f;
+    int last = 0x7fffffff;
+    auto inside = [&](float l, int i) { return l > thr || (l == thr && begin + i <= last); };
+    // f on four of this lane's tokens at a time, and the first one's index (-infinity beyond the row)
+    auto each = [&](auto&& f) {
+        for (int i = s0 + 4 * lane; i < s0 + a.seg; i += 128) {
+            const float4 v = *reinterpret_cast<const float4*>(vals + i);
+            const float l[4] = {v.x, v.y, v.z, v.w};
+            f(l, i);
+        }
+    };
+    int buf = 0;
+#pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         const bool mass = pass == 1;
         if (!(mass ? by_p : by_k)) continue;
-        // what a token adds: one, or its weight; the tokens at a top-k threshold add the weight of q of them once
-        auto adds = [&](float l) -> u64 {
-            if (!mass) return 1;
-            return order_key(l) > kt || q == ~0ull ? weigh.units(l) : 0;
-        };
-        auto tie_mass = [&](float l) -> u64 { return q * weigh.units(l); };
-        const bool tied = mass && q != ~0ull;   // a top-k threshold is set
-        float kt_val = 0.f;
-        if (tied) kt_val = __uint_as_float(kt & 0x80000000u ? kt ^ 0x80000000u : ~kt);
-        auto clear = [&]() {
-            for (int i = tid; i < kBins; i += kST) S.hist[i] = 0;
+        // steps of 1/128 of a temperature for masses, of 1/64 for counts: a few hundred tokens at most in the
+        // bins that matter
+        const Coarse coarse{mx, (float)fmin(fmax(mass ? inv * 128.0 : 64.0, 1e-38), 1e38)};
+        u64 target = (u64)K, before = 0, own = 0;
+        uint32_t bin = 0, lo = 0, hi = 0;
+        bool found = false;
+        // The first histogram; if its bin holds too many tokens to order at once, the bits of the keys in it.
+#pragma unroll 1
+        for (int round = 0;; ++round) {
+            const int shift = round ? max(0, 32 - __clz(hi - lo) - 11) : 0;
+            uint4* h = reinterpret_cast<uint4*>(S.hist[buf]);
+            h[tid] = make_uint4(0, 0, 0, 0);
+            if (mass) h[kST + tid] = make_uint4(0, 0, 0, 0);
+            if (tid == 0) S.list_n = 0;
             __syncthreads();
-        };
-        clear();
-        u64 total = 0;
-        for (int i = tid; i < cnt; i += kST) {
-            const float l = vals[i];
-            if (l == kNegInf || (mass && order_key(l) < kt)) continue;
-            const u64 v = adds(l);
-            if (v) atomicAdd(&S.hist[coarse(l)], v);
-            total += v;
-        }
-        if (tied && r == 0 && tid == 0) {
-            const u64 v = tie_mass(kt_val);
-            atomicAdd(&S.hist[coarse(kt_val)], v);
-            total += v;
-        }
-        u64 target = (u64)K;
-        if (mass) {   // p of the total
+            auto bin_of = [&](float l) -> uint32_t {   // kBins or more: not in this round
+                if (round == 0) return coarse(l);
+                const uint32_t k = order_key(l);
+                return k - lo <= hi - lo ? (hi - k) >> shift : kAll;
+            };
+            if (mass) {
+                each([&](const float (&l)[4], int i) {
+                    uint32_t b[4];
+                    bool any = false;
 #pragma unroll
-            for (int m = 16; m >= 1; m >>= 1) total += __shfl_xor_sync(kAll, total, m);
-            if (lane == 0) S.wsum[warp] = total;
-            __syncthreads();
-            total = 0;
-            for (int w = 0; w < kSW; ++w) total += S.wsum[w];
-            if (tid < C) cl.map_shared_rank(S.mass, tid)[r] = total;
-            cl.sync();
-            total = 0;
-            for (int p = 0; p < C; ++p) total += S.mass[p];
-            target = max(1ull, (u64)__double2ll_ru(fmax((double)P, 0.0) * (double)total));
-            target = min(target, total);
-        }
-        uint32_t bin;
-        u64 before;
-        if (!find_bin(cl, S, target, bin, before)) continue;   // top-k of more tokens than there are
-        // the keys of that bin
-        uint32_t lo = 0xffffffffu, hi = 0;
-        for (int i = tid; i < cnt; i += kST) {
-            const float l = vals[i];
-            if (l != kNegInf && coarse(l) == bin) {
-                const uint32_t k = order_key(l);
-                if (!mass || k >= kt) lo = min(lo, k), hi = max(hi, k);
+                    for (int e = 0; e < 4; ++e) {
+                        b[e] = inside(l[e], i + e) ? bin_of(l[e]) : kAll;
+                        any |= b[e] < kBins;
+                    }
+                    if (!__any_sync(kAll, any)) return;
+                    u64 v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = weigh.units(l[e]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (b[e] < kBins && v[e]) {
+                            const uint32_t x = (uint32_t)v[e];
+                            const uint32_t old = atomicAdd(&S.hist[buf][0][b[e]], x);
+                            const uint32_t y = (uint32_t)(v[e] >> 32) + (old + x < x);   // with the carry
+                            if (y) atomicAdd(&S.hist[buf][1][b[e]], y);
+                        }
+                    }
+                });
+            } else {
+                each([&](const float (&l)[4], int i) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t b = l[e] != kNegInf ? bin_of(l[e]) : kAll;
+                        if (b < kBins) atomicAdd(&S.hist[buf][0][b], 1u);
+                    }
+                });
             }
-        }
-        lo = __reduce_min_sync(kAll, lo);
-        hi = __reduce_max_sync(kAll, hi);
-        if (lane == 0) S.wlo[warp] = lo, S.whi[warp] = hi;
-        __syncthreads();
-        for (int w = 0; w < kSW; ++w) lo = min(lo, S.wlo[w]), hi = max(hi, S.whi[w]);
-        if (tid < C) {
-            cl.map_shared_rank(S.klo, tid)[r] = lo;
-            cl.map_shared_rank(S.khi, tid)[r] = hi;
-        }
-        cl.sync();
-        for (int p = 0; p < C; ++p) lo = min(lo, S.klo[p]), hi = max(hi, S.khi[p]);
-        while (lo < hi) {
-            const int shift = max(0, 32 - __clz(hi - lo) - 11);
-            clear();
-            for (int i = tid; i < cnt; i += kST) {
-                const float l = vals[i];
-                const uint32_t k = order_key(l);
-                if (k >= lo && k <= hi && l != kNegInf && (!mass || k >= kt)) {
-                    const u64 v = adds(l);
-                    if (v) atomicAdd(&S.hist[(hi - k) >> shift], v);
+            __syncthreads();
+            push_groups<C>(cl, S, buf, mass);
+            cl.sync();
+            if (round == 0) {
+                u64 inc, mine;
+                const u64 total = group_scan<C>(S, buf, lane, inc, mine);
+                if (mass) {   // p of the total
+                    target = max(1ull, (u64)__double2ll_ru(fmax((double)P, 0.0) * (double)total));
+                    target = min(target, total);
+                } else if (total < target) {   // top-k of more tokens than there are
+                    buf ^= 1;
+                    break;
                 }
             }
-            if (tied && r == 0 && tid == 0 && kt >= lo && kt <= hi) atomicAdd(&S.hist[(hi - kt) >> shift], tie_mass(kt_val));
-            uint32_t sub;
+            uint32_t b;
             u64 rel;
-            if (!find_bin(cl, S, target - before, sub, rel)) break;
+            find_bin<C>(S, buf, mass, target - before, b, rel, own);
+            buf ^= 1;
             before += rel;
-            hi -= sub << shift;
-            lo = max(lo, hi - ((1u << shift) - 1u));
+            found = true;
+            if (round == 0) {
+                // the tokens of the bin: a list of the first few, and the range of their keys
+                bin = b;
+                uint32_t l0 = 0xffffffffu, h0 = 0;
+                each([&](const float (&l)[4], int i) {
+                    bool in[4], any = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        in[e] = coarse(l[e]) == bin && inside(l[e], i + e);
+                        any |= in[e];
+                    }
+                    if (!__any_sync(kAll, any)) return;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (in[e]) {
+                            const uint32_t k = order_key(l[e]);
+                            l0 = min(l0, k), h0 = max(h0, k);
+                            const uint32_t at = atomicAdd(&S.list_n, 1u);   // any order: they are sorted
+                            if (at < kList / C) S.list[at] = order_of(k, begin + i + e);
+                        }
+                    }
+                });
+                l0 = __reduce_min_sync(kAll, l0);
+                h0 = __reduce_max_sync(kAll, h0);
+                if (lane == 0) S.wlo[warp] = l0, S.whi[warp] = h0;
+                __syncthreads();
+#pragma unroll
+                for (int w = 0; w < kSW; ++w) l0 = min(l0, S.wlo[w]), h0 = max(h0, S.whi[w]);
+                if (tid < C) {
+                    cl.map_shared_rank(S.klo, tid)[r] = l0;
+                    cl.map_shared_rank(S.khi, tid)[r] = h0;
+                    cl.map_shared_rank(S.listed, tid)[r] = S.list_n;
+                }
+                cl.sync();
+                bool fits = true;
+#pragma unroll
+                for (int p = 0; p < C; ++p) {
+                    l0 = min(l0, S.klo[p]), h0 = max(h0, S.khi[p]);
+                    fits &= S.listed[p] <= kList / C;
+                }
+                lo = l0, hi = h0;
+                if (fits) {
+                    const int p = tid / (kList / C), j = tid % (kList / C);
+                    u64 v = (uint32_t)j < S.listed[p] ? cl.map_shared_rank(S.list, p)[j] : 0;
+                    if (C > 1) cl.sync();   // the peers have read this CTA's list
+                    else __syncthreads();
+                    v = sort_desc(S, v);
+                    const float l = key_value((uint32_t)(v >> 32));
+                    const u64 w = !v ? 0 : mass ? weigh.units(l) : 1;
+                    u64 inc = warp_scan(w, lane);
+                    if (lane == 31) S.wsum[warp] = inc;
+                    __syncthreads();
+                    inc += before;
+#pragma unroll
+                    for (int x = 0; x < kSW; ++x)
+                        if (x < warp) inc += S.wsum[x];
+                    if (w && inc >= target && inc - w < target) S.list[0] = v;   // one thread
+                    __syncthreads();
+                    const u64 at = S.list[0];
+                    thr = key_value((uint32_t)(at >> 32));
+                    last = (int)~(uint32_t)at;
+                    found = false;
+                    break;
+                }
+            } else {
+                hi -= b << shift;
+                lo = max(lo, hi - ((1u << shift) - 1u));
+            }
+            if (lo >= hi) break;
         }
-        kt = hi;
-        if (mass) {
-            const u64 w = weigh.units(__uint_as_float(kt & 0x80000000u ? kt ^ 0x80000000u : ~kt));
-            q = w ? (target - before + w - 1) / w : 1;
-        } else {
-            q = target - before;
+        if (found) {
+            // one key holds the prefix's end: its first tokens in index order complete the target
+            const float at = key_value(hi);
+            const u64 w = mass ? weigh.units(at) : 1;
+            const u64 q = (target - before + w - 1) / w;
+            if (q >= own / w) {   // all of those that were left; at an earlier threshold its last index stays
+                last = at == thr ? last : 0x7fffffff;
+            } else {
+                uint32_t t = 0;
+                each([&](const float (&l)[4], int i) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) t += l[e] == at;
+                });
+                t = __reduce_add_sync(kAll, t);
+                if (lane == 0) S.wtie[warp] = t;
+                __syncthreads();
+                uint32_t mine = 0, all = 0;
+#pragma unroll
+                for (int x = 0; x < kSW; ++x) {
+                    if (x < warp) mine += S.wtie[x];
+                    all += S.wtie[x];
+                }
+                if (tid < C) cl.map_shared_rank(S.ties, tid)[r] = all;
+                cl.sync();
+#pragma unroll
+                for (int p = 0; p < C; ++p)
+                    if (p < r) mine += S.ties[p];
+                if (mine < q && mine + t >= q) {   // the q-th one is this warp's
+                    u64 n = mine;
+                    for (int i = s0 + lane; i < s0 + a.seg; i += 32) {
+                        const uint32_t m = __ballot_sync(kAll, vals[i] == at);
+                        if (n + __popc(m) >= q) {
+                            if ((m >> lane & 1u) && n + __popc(m & ((1u << lane) - 1u)) + 1 == q)
+                                for (int p = 0; p < C; ++p) *cl.map_shared_rank(&S.tie_at, p) = begin + i;
+                            break;
+                        }
+                        n += __popc(m);
+                    }
+                }
+                cl.sync();
+                last = S.tie_at;
+            }
+            thr = at;
         }
     }
 
-    // ---- the tokens at the threshold, in index order: how many lie before this warp's
-    const int seg = ((cnt + kSW - 1) / kSW + 31) & ~31;
-    const int s0 = min(cnt, warp * seg), s1 = min(cnt, s0 + seg);
-    u64 tie0 = 0;
-    const bool limited = q != ~0ull;
-    if (limited) {
-        uint32_t t = 0;
-        for (int i = s0 + lane; i < s1; i += 32) t += order_key(vals[i]) == kt;
-        t = __reduce_add_sync(kAll, t);
-        if (lane == 0) S.wtie[warp] = t;
-        __syncthreads();
-        uint32_t mine = 0, all = 0;
-        for (int w = 0; w < kSW; ++w) {
-            if (w < warp) mine += S.wtie[w];
-            all += S.wtie[w];
+    // weights of this lane's four tokens from i on, those that are kept
+    auto kept = [&](int i, double (&w)[4]) {
+        const float4 v = *reinterpret_cast<const float4*>(vals + i);
+        const float l[4] = {v.x, v.y, v.z, v.w};
+        bool in[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) in[e] = inside(l[e], i + e);
+        if (!__any_sync(kAll, in[0] || in[1] || in[2] || in[3])) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = 0.0;
+            return;
         }
-        if (tid < C) cl.map_shared_rank(S.ties, tid)[r] = all;
-        cl.sync();
-        tie0 = mine;
-        for (int p = 0; p < r; ++p) tie0 += S.ties[p];
-    }
-    // weight of element i (this lane's of a step of 32) if it is kept, else 0; counts ties on
-    auto kept = [&](int i, u64& tie) -> double {
-        const float l = i < s1 ? vals[i] : kNegInf;
-        const uint32_t k = order_key(l);
-        bool in = l != kNegInf && k >= kt;
-        if (limited) {
-            const bool at = i < s1 && k == kt;
-            const uint32_t b = __ballot_sync(kAll, at);
-            if (at && tie + __popc(b & ((1u << lane) - 1u)) >= q) in = false;
-            tie += __popc(b);
-        }
-        if (!__any_sync(kAll, in)) return 0.0;
-        const double w = in ? weigh(l) : 0.0;
-        return by_m && w < minw ? 0.0 : w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = weigh(l[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (!in[e] || (by_m && w[e] < minw)) w[e] = 0.0;
     };
 
     // ---- their total, and each warp's share
-    u64 sum = 0, tie = tie0;
-    for (int i0 = s0; i0 < s1; i0 += 32) sum += (u64)__double2ll_rn(kept(i0 + lane, tie) * kOne);
+    u64 sum = 0;
+    if (by_k || by_p) {
+        // few of many, as a rule: the warp gathers them and takes the exponentials of 32 at a time
+        // (in the histogram that was not the last: its peers' reads ended before a barrier)
+        float* queue = reinterpret_cast<float*>(S.hist[buf]) + warp * 160;
+        int n = 0;
+        auto flush = [&](bool in) {
+            const double w = weigh(in ? queue[lane] : mx);
+            if (in && !(by_m && w < minw)) sum += Weigh::to_units(w);
+        };
+        __syncthreads();
+        each([&](const float (&l)[4], int i) {
+            bool in[4];
+            int mine = 0;
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(kAll, sum, m);
+            for (int e = 0; e < 4; ++e) {
+                in[e] = inside(l[e], i + e);
+                mine += in[e];
+            }
+            if (!__any_sync(kAll, mine)) return;
+            int at = n;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t m = __ballot_sync(kAll, in[e]);
+                if (in[e]) queue[at + __popc(m & ((1u << lane) - 1u))] = l[e];
+                at += __popc(m);
+            }
+            n = at;
+            __syncwarp();
+            while (n >= 32) {   // the last 32 of the queue
+                const float v = queue[n - 32 + lane];
+                n -= 32;
+                const double w = weigh(v);
+                if (!(by_m && w < minw)) sum += Weigh::to_units(w);
+            }
+            __syncwarp();
+        });
+        flush(lane < n);
+    } else {
+#pragma unroll 2
+        for (int i = s0 + 4 * lane; i < s0 + a.seg; i += 128) {
+            double w[4];
+            kept(i, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += Weigh::to_units(w[e]);
+        }
+    }
+    sum = warp_sum(sum);
     __syncthreads();   // S.wsum of find_bin has been read
     if (lane == 0) S.wsum[warp] = sum;
     __syncthreads();
     u64 base = 0, all = 0;
+#pragma unroll
     for (int w = 0; w < kSW; ++w) {
         if (w < warp) base += S.wsum[w];
         all += S.wsum[w];
     }
-    if (tid < C) cl.map_shared_rank(S.slice_tot, tid)[r] = all;
-    cl.sync();
-    u64 total = 0;
-    for (int p = 0; p < C; ++p) {
-        if (p < r) base += S.slice_tot[p];
-        total += S.slice_tot[p];
+    u64 total = all;
+    if (C > 1) {
+        if (tid < C) cl.map_shared_rank(S.slice_tot, tid)[r] = all;
+        cl.sync();
+        total = 0;
+#pragma unroll
+        for (int p = 0; p < C; ++p) {
+            if (p < r) base += S.slice_tot[p];
+            total += S.slice_tot[p];
+        }
     }
     const double norm = kOne / (double)total;
 
@@ -384,20 +606,26 @@ __global__ void __launch_bounds__(kST) k_sample(SampleArgs a) {
     const u64 target = !(x > 0.0) ? 0 : x >= (double)total ? total - 1 : min((u64)x, total - 1);
     if (target >= base && target < base + sum) {   // one warp of the cluster
         u64 run = base;
-        tie = tie0;
-        for (int i0 = s0; i0 < s1; i0 += 32) {
-            const double w = kept(i0 + lane, tie);
-            u64 inc = (u64)__double2ll_rn(w * kOne);
+        for (int i = s0 + 4 * lane; i < s0 + a.seg; i += 128) {
+            double w[4];
+            kept(i, w);
+            u64 mine = 0;
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const u64 o = __shfl_up_sync(kAll, inc, m);
-                if (lane >= m) inc += o;
-            }
+            for (int e = 0; e < 4; ++e) mine += Weigh::to_units(w[e]);
+            const u64 inc = warp_scan(mine, lane);
             const uint32_t b = __ballot_sync(kAll, run + inc > target);
             if (b) {
                 if (lane == __ffs(b) - 1) {
-                    a.token[row] = begin + i0 + lane;
-                    if (a.prob) a.prob[row] = (float)(w * norm);
+                    u64 at = run + inc - mine;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const u64 next = at + Weigh::to_units(w[e]);
+                        if (at <= target && next > target) {
+                            a.token[row] = begin + i + e;
+                            if (a.prob) a.prob[row] = (float)(w[e] * norm);
+                        }
+                        at = next;
+                    }
                 }
                 break;
             }
@@ -405,12 +633,33 @@ __global__ void __launch_bounds__(kST) k_sample(SampleArgs a) {
         }
     }
     if (probs) {
-        tie = tie0;
-        for (int i0 = s0; i0 < s1; i0 += 32) {
-            const double w = kept(i0 + lane, tie);
-            if (i0 + lane < s1) probs[i0 + lane] = (float)(w * norm);
+        for (int i = s0 + 4 * lane; i < s0 + a.seg; i += 128) {
+            double w[4];
+            kept(i, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < cnt) probs[i + e] = (float)(w[e] * norm);
         }
     }
+}
+
+template <bool BF, int C>
+static cudaError_t sample_launch(const SampleArgs& a, int n, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(k_sample<BF, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSampleMaxVocab / kMaxCluster * 4);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n * C);
+    cfg.blockDim = dim3(kST);
+    cfg.dynamicSmemBytes = (size_t)kSW * a.seg * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = C;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_sample<BF, C>, a);
 }
 
 cudaError_t launch_sample(SampleArgs a, bool bf16, int n, cudaStream_t st) {
@@ -418,23 +667,17 @@ cudaError_t launch_sample(SampleArgs a, bool bf16, int n, cudaStream_t st) {
     int C = 1;
     while (C < kMaxCluster && (a.V + C - 1) / C > 8192) C *= 2;
     a.slice = (((a.V + C - 1) / C) + 7) & ~7;
-    const size_t smem = (size_t)a.slice * sizeof(float);
-    const void* fn = bf16 ? reinterpret_cast<const void*>(k_sample<true>) : reinterpret_cast<const void*>(k_sample<false>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSampleMaxVocab / kMaxCluster * 4));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)n * C);
-    cfg.blockDim = dim3(kST);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)C;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    void* args[] = {&a};
-    return cudaLaunchKernelExC(&cfg, fn, args);
+    a.seg = ((a.slice + kSW - 1) / kSW + 127) & ~127;
+    if (bf16) {
+        if (C == 1) return sample_launch<true, 1>(a, n, st);
+        if (C == 2) return sample_launch<true, 2>(a, n, st);
+        if (C == 4) return sample_launch<true, 4>(a, n, st);
+        return sample_launch<true, 8>(a, n, st);
+    }
+    if (C == 1) return sample_launch<false, 1>(a, n, st);
+    if (C == 2) return sample_launch<false, 2>(a, n, st);
+    if (C == 4) return sample_launch<false, 4>(a, n, st);
+    return sample_launch<false, 8>(a, n, st);
 }
 
 }  // namespace ds4
