@@ -70,6 +70,7 @@ struct ProjectArgs {
     int bn, row_tiles, cap, kblocks, tiles, split, stages;   // set by the launcher
 };
 struct ProjectWork {            // layout of the caller's work buffer
+    bool pair;
     int bn, row_tiles, cap;
     size_t off_entry, off_t, total;
 };

@@ -186,6 +186,39 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
     }
 }
 
+// One warp's share of a tile to out: this lane's output feature o (TMEM lane),
+// the rows r0 .. r0 + rows - 1 as columns from taddr on.  Two lanes exchange
+// half of their values, so that a lane stores two features of one row at once.
+// Not ok (a wait ran out): NaN.
+__device__ __forceinline__ void store_tile(const ProjectArgs& a, uint32_t taddr, int o, int lane, int r0, int rows, bool ok) {
+    __nv_bfloat16* dst = a.out + (size_t)r0 * a.fout;
+    const bool pairs = (a.fout & 1) == 0;
+    for (int c0 = 0; c0 < rows; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld_32x16(taddr + c0, v);
+        tmem_wait_ld();
+        if (!ok) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
+        }
+        if (pairs) {
+            const int odd = lane & 1;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+                // an even lane takes row j, an odd one row j + 1
+                const uint32_t mine = odd ? v[j + 1] : v[j], other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                const uint32_t w = pack_bf16x2(__uint_as_float(odd ? other : mine), __uint_as_float(odd ? mine : other));
+                if (o < a.fout && c0 + j + odd < rows)
+                    *reinterpret_cast<uint32_t*>(dst + (size_t)(c0 + j + odd) * a.fout + (o & ~1)) = w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (o < a.fout && c0 + j < rows) dst[(size_t)(c0 + j) * a.fout + o] = __float2bfloat16_rn(__uint_as_float(v[j]));
+        }
+    }
+}
+
 // ---------------------------------------------------------------- the GEMM
 // A block of the K axis is 64 columns: TMA brings 128 rows of W (or of B_a) and
 // bn rows of x (or of t) into a ring of stages, one thread issues the MMAs,
@@ -360,17 +393,7 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
                     for (int j = 0; j < 16; ++j) part[(c0 + j) * kPM] = ok ? __uint_as_float(v[j]) : __int_as_float(0x7fffffff);
                 }
             } else {
-                __nv_bfloat16* dst = a.out + (size_t)r0 * a.fout + o;
-                for (int c0 = 0; c0 < rows; c0 += 16) {
-                    uint32_t v[16];
-                    tmem_ld_32x16(taddr + c0, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (o < a.fout && c0 + j < rows)
-                            dst[(size_t)(c0 + j) * a.fout] =
-                                __float2bfloat16_rn(ok ? __uint_as_float(v[j]) : __int_as_float(0x7fffffff));
-                }
+                store_tile(a, taddr, o, lane, r0, rows, ok);
             }
             tc_fence_before();
             __syncwarp();
@@ -406,6 +429,232 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
     }
 }
 
+// ---------------------------------------------------------------- the GEMM by CTA pairs
+// Many tiles: what bounds them is the L2's rate into the SMs (about 9 TB/s
+// here), so the tile is as large as the tensor memory of two SMs holds: 512
+// output features x bn rows per pair, 96 KB per K block of 16.8 MFLOP (a
+// single CTA's 128 x 256 tile needs three times that per FLOP, and measured
+// 790 TFLOP/s).  cta_group::2 MMAs (M 256): CTA r of the pair holds rows
+// 128 r .. of each 256 features and half of x's rows; the leader's thread
+// issues for both.  Both accumulators (2 x bn columns) are in use, so a tile's
+// epilogue is not overlapped; eight warps drain it, four per accumulator.
+struct PairSmem {
+    uint64_t full[kPMaxStages], empty[kPMaxStages];
+    uint64_t accF, accE[2];
+    uint32_t tmem;
+    volatile uint32_t abort;
+};
+constexpr int kPairThreads = 384;   // warps: 0 TMA, 1 MMA (leader), 2 TMEM, 4..11 epilogue
+
+__device__ __forceinline__ uint32_t map_rank0(uint32_t addr) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+// Tiled loads of a pair: into this CTA's shared memory, completing on the leader's barrier.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(da), "l"(db), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs when the MMAs issued so far have completed.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+    const uint16_t both = 3;
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_addr(bar)),
+                 "h"(both)
+                 : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+    k_project_pair(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
+                   const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapT, ProjectArgs a) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ PairSmem S;
+    unsigned char* st = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    cg::cluster_group cl = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = (int)cl.block_rank();
+    const int half = a.bn / 2;
+    const int stage_bytes = 2 * kPStageA + half * kPK * 2;
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    uint32_t* err = &g_project_err;
+    auto stop = [&]() {   // a wait ran out: both CTAs of the pair end
+        S.abort = 1;
+        *const_cast<volatile uint32_t*>(cl.map_shared_rank(const_cast<uint32_t*>(&S.abort), r ^ 1)) = 1;
+    };
+
+    if (tid == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], 1);
+        }
+        mbar_init(&S.accF, 1);
+        for (int m = 0; m < 2; ++m) mbar_init(&S.accE[m], 8);
+        S.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&S.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    __syncwarp();
+    tc_fence_before();
+    cl.sync();   // the barriers of both CTAs exist before anything arrives at them
+    tc_fence_after();
+    const uint32_t tmem = S.tmem;
+    const int R16 = (a.rank + 15) & ~15;
+    const bool one_block = 2 * R16 <= kPK;
+    const int per_entry = one_block ? 1 : 2 * ((R16 + kPK - 1) / kPK);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool waited = false;
+            auto slot = [&]() -> int {
+                const int s = it % a.stages;
+                if (!mbar_wait(&S.empty[s], ((it / a.stages) & 1) ^ 1, err)) {
+                    stop();
+                    return -1;
+                }
+                if (r == 0) mbar_arrive_expect_tx(&S.full[s], 2 * stage_bytes);   // what both CTAs bring
+                ++it;
+                return s;
+            };
+            for (int tile = first; tile < a.tiles && !S.abort; tile += step) {
+                const int o0 = tile / a.row_tiles * (4 * kPM) + r * kPM, rt = tile % a.row_tiles, r0 = rt * a.bn + r * half;
+                for (int kb = 0; kb < a.kblocks; ++kb) {
+                    const int s = slot();
+                    if (s < 0) break;
+                    const uint32_t p = smem_addr(st + s * stage_bytes), bar = map_rank0(smem_addr(&S.full[s]));
+                    pair_load_2d(p, &mapW, kb * kPK, o0, bar);
+                    pair_load_2d(p + kPStageA, &mapW, kb * kPK, o0 + 2 * kPM, bar);
+                    pair_load_2d(p + 2 * kPStageA, &mapX, kb * kPK, r0, bar);
+                }
+                if (a.counts) {
+                    if (!waited) {
+                        griddep_wait();
+                        asm volatile("fence.proxy.async.global;" ::: "memory");
+                        waited = true;
+                    }
+                    const int count = __ldcg(a.counts + rt);
+                    for (int j = 0; j < count && !S.abort; ++j) {
+                        const int ad = __ldcg(a.entry + rt * a.cap + j);
+                        const int trow = (rt * a.cap + j) * a.bn + r * half;
+                        for (int b = 0; b < per_entry; ++b) {
+                            const int s = slot();
+                            if (s < 0) break;
+                            const uint32_t p = smem_addr(st + s * stage_bytes), bar = map_rank0(smem_addr(&S.full[s]));
+                            const int c = (b >> 1) * kPK, piece = b & 1;
+                            pair_load_3d(p, &mapB, c, o0, ad, bar);
+                            pair_load_3d(p + kPStageA, &mapB, c, o0 + 2 * kPM, ad, bar);
+                            pair_load_2d(p + 2 * kPStageA, &mapT, piece * R16 + c, trow, bar);
+                        }
+                    }
+                }
+            }
+            if (S.abort && r == 0) {   // no copy of either CTA may be in flight when the pair leaves
+                const uint32_t n = it < (uint32_t)a.stages ? it : (uint32_t)a.stages;
+                for (uint32_t i = it - n; i < it; ++i) mbar_wait(&S.full[i % a.stages], (i / a.stages) & 1, err);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && r == 0) {
+            const uint32_t idesc = umma_idesc_bf16(2 * kPM, a.bn);
+            uint32_t it = 0, use = 0;
+            bool waited = false;
+            for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
+                const int rt = tile % a.row_tiles;
+                uint32_t fresh = 3;   // accumulators not yet begun
+                auto block = [&](int na, int b0, bool again) -> bool {
+                    const int s = it % a.stages;
+                    if (!again) {
+                        if (!mbar_wait(&S.full[s], (it / a.stages) & 1, err)) { stop(); return false; }
+                        tc_fence_after();
+                    }
+                    const uint32_t p = smem_addr(st + s * stage_bytes);
+                    const uint64_t db = umma_desc_sw128(p + 2 * kPStageA);
+                    for (int m = 0; m < 2; ++m) {
+                        if (fresh >> m & 1u) {   // the last tile's sums have been read
+                            if (!mbar_wait(&S.accE[m], (use & 1) ^ 1, err)) { stop(); return false; }
+                            tc_fence_after();
+                        }
+                        const uint64_t da = umma_desc_sw128(p + m * kPStageA);
+                        for (int k = 0; k < na; ++k) {
+                            pair_mma(tmem + m * a.bn, da + 2 * k, db + 2 * (b0 + k), idesc, !(fresh >> m & 1u));
+                            fresh &= ~(1u << m);
+                        }
+                    }
+                    return true;
+                };
+                auto next = [&]() {
+                    pair_commit(&S.empty[it % a.stages]);
+                    ++it;
+                };
+                for (int kb = 0; kb < a.kblocks; ++kb) {
+                    if (!block(kPK / 16, 0, false)) break;
+                    next();
+                }
+                if (a.counts && !S.abort) {
+                    if (!waited) {
+                        griddep_wait();
+                        waited = true;
+                    }
+                    const int count = __ldcg(a.counts + rt);
+                    for (int j = 0; j < count && !S.abort; ++j)
+                        for (int b = 0; b < per_entry; ++b) {
+                            if (one_block) {
+                                if (!block(R16 / 16, 0, false) || !block(R16 / 16, R16 / 16, true)) break;
+                            } else if (!block(min(kPK, R16 - (b >> 1) * kPK) / 16, 0, false)) {
+                                break;
+                            }
+                            next();
+                        }
+                }
+                pair_commit(&S.accF);
+            }
+        }
+    } else if (warp >= 4) {
+        const int qd = warp & 3, m = (warp - 4) >> 2;   // TMEM lanes 32 qd .., accumulator m
+        uint32_t use = 0;
+        for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
+            if (!mbar_wait(&S.accF, use & 1, err)) stop();
+            const bool ok = !S.abort;
+            tc_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + m * a.bn;
+            const int o = tile / a.row_tiles * (4 * kPM) + m * (2 * kPM) + r * kPM + 32 * qd + lane, r0 = tile % a.row_tiles * a.bn;
+            store_tile(a, taddr, o, lane, r0, min(a.bn, a.n - r0), ok);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank0(smem_addr(&S.accE[m])))
+                             : "memory");
+        }
+    }
+    if (a.counts) griddep_wait();
+    __syncwarp();
+    tc_fence_before();
+    cl.sync();   // neither CTA leaves while the other may still read its operands or signal its barriers
+    if (warp == 2) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
 // ---------------------------------------------------------------- host side
 static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
@@ -433,26 +682,34 @@ static cudaError_t encode(CUtensorMap* map, const void* base, uint64_t cols, uin
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Rows per tile: up to 128 rows one tile, as narrow as they allow (the N side
-// of an MMA is a multiple of 16).  More rows: the width whose tiles fill the
-// SMs best; a wave of tiles takes time in proportion to the width plus a
-// start-up worth about 16 columns.
-static int project_bn(int n, int fout) {
-    constexpr int n_sm = 148;   // the size of the work buffer must not depend on the current device
-    if (n <= 128) return (n + 15) & ~15;
-    const int64_t ot = (fout + kPM - 1) / kPM;
-    int best = 256;
-    int64_t cost = INT64_MAX;
-    for (int bn = 256; bn >= 64; bn -= 16) {
-        const int64_t tiles = ot * ((n + bn - 1) / bn), c = (tiles + n_sm - 1) / n_sm * (bn + 16);
-        if (c < cost) cost = c, best = bn;
+// Rows per tile (the N side of an MMA: a multiple of 16, up to 256), and
+// whether CTA pairs take 512 output features of them.  Up to 128 rows: one
+// tile, as narrow as they allow.  More: what ends first when each round of
+// tiles takes the time that the L2 needs to bring its operands, in proportion
+// to the features and rows that an SM loads (128 + bn alone, 256 + bn / 2 in a
+// pair; 64 more for a round's start and end).  4096 x 4096 x 4096: pairs of 240
+// rows, two rounds, against four of 256 x 128.
+static bool project_tile(int n, int fout, int& bn) {
+    constexpr int64_t n_sm = 148;   // the size of the work buffer must not depend on the current device
+    if (n <= 128) {
+        bn = (n + 15) & ~15;
+        return false;
     }
-    return best;
+    bool pair = false;
+    int64_t cost = INT64_MAX;
+    for (int b = 256; b >= 64; b -= 16) {
+        const int64_t rows = (n + b - 1) / b;
+        const int64_t alone = (rows * ((fout + kPM - 1) / kPM) + n_sm - 1) / n_sm * (128 + b + 64);
+        const int64_t both = (rows * ((fout + 4 * kPM - 1) / (4 * kPM)) + n_sm / 2 - 1) / (n_sm / 2) * (256 + b / 2 + 64);
+        if (alone < cost) cost = alone, bn = b, pair = false;
+        if (both < cost) cost = both, bn = b, pair = true;
+    }
+    return pair;
 }
 
 ProjectWork project_work(int n, int fout, int n_adapters, int rank) {
     ProjectWork w{};
-    w.bn = project_bn(n, fout);
+    w.pair = project_tile(n, fout, w.bn);
     w.row_tiles = (n + w.bn - 1) / w.bn;
     w.cap = n_adapters < w.bn ? n_adapters : w.bn;
     auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
@@ -468,20 +725,21 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     p.row_tiles = wk.row_tiles;
     p.cap = wk.cap;
     p.kblocks = (p.fin + kPK - 1) / kPK;
-    p.tiles = (p.fout + kPM - 1) / kPM * p.row_tiles;
+    const int features = wk.pair ? 4 * kPM : kPM;
+    p.tiles = (p.fout + features - 1) / features * p.row_tiles;
     // Few tiles: several CTAs share one, as many as leave each four blocks of W and find an SM of their own.
     p.split = 1;
-    while (p.split < 8 && (int64_t)p.tiles * p.split * 2 <= n_sm && p.kblocks >= p.split * 2 * 4) p.split *= 2;
-    const int stage = kPStageA + p.bn * kPK * 2;
+    while (!wk.pair && p.split < 8 && (int64_t)p.tiles * p.split * 2 <= n_sm && p.kblocks >= p.split * 2 * 4) p.split *= 2;
+    const int stage = wk.pair ? 2 * kPStageA + p.bn / 2 * kPK * 2 : kPStageA + p.bn * kPK * 2;
     p.stages = kPSmem / stage < kPMaxStages ? kPSmem / stage : kPMaxStages;
     const int smem = 1024 + p.stages * stage;   // the partial sums of a split tile (512 bytes per row) fit as well
 
     CUtensorMap mW, mX, mB = {}, mT = {};
     cudaError_t e = encode(&mW, W, p.fin, p.fout, 1, 2, kPM);
-    if (e == cudaSuccess) e = encode(&mX, s.x, p.fin, p.n, 1, 2, p.bn);
+    if (e == cudaSuccess) e = encode(&mX, s.x, p.fin, p.n, 1, 2, wk.pair ? p.bn / 2 : p.bn);
     if (e == cudaSuccess && p.counts) e = encode(&mB, B, p.rank, p.fout, s.n_adapters, 3, kPM);
     if (e == cudaSuccess && p.counts)
-        e = encode(&mT, s.t, t_cols(p.rank), (uint64_t)p.row_tiles * p.cap * p.bn, 1, 2, p.bn);
+        e = encode(&mT, s.t, t_cols(p.rank), (uint64_t)p.row_tiles * p.cap * p.bn, 1, 2, wk.pair ? p.bn / 2 : p.bn);
     if (e != cudaSuccess) return e;
 
     if (p.counts) {
@@ -499,11 +757,14 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(k_project, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem + 1024);
+    const auto kernel = wk.pair ? k_project_pair : k_project;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem + 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.split > 1 ? p.tiles * p.split : p.tiles < n_sm ? p.tiles : n_sm));
-    cfg.blockDim = dim3(kPThreads);
+    const int tiles_at_once = wk.pair ? n_sm / 2 : n_sm;
+    const int tiles = p.split > 1 || p.tiles < tiles_at_once ? p.tiles : tiles_at_once;
+    cfg.gridDim = dim3((unsigned)(tiles * (wk.pair ? 2 : p.split)));
+    cfg.blockDim = dim3(wk.pair ? kPairThreads : kPThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
@@ -521,7 +782,7 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     }
     cfg.attrs = at;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, k_project, mW, mX, mB, mT, p);
+    return cudaLaunchKernelEx(&cfg, kernel, mW, mX, mB, mT, p);
 }
 
 cudaError_t read_project_error(uint32_t* code, cudaStream_t st) {
