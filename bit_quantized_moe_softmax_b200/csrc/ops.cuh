@@ -57,7 +57,7 @@ struct ShrinkArgs {
     const float* scale;         // [n_adapters]
     const int32_t* ids;         // [n]
     int n, fin, n_adapters, rank;
-    int bn, cap;                // rows per tile, entries per tile (set by the launcher)
+    int bn, cap, split;         // rows per tile, entries per tile, CTAs per 64 rows (set by the launcher)
     int32_t* counts;            // [tiles] distinct adapters of a tile
     int32_t* entry;             // [tiles][cap] their indices
     __nv_bfloat16* t;           // [tiles][cap][bn][2 * rank rounded to 16]

@@ -52,23 +52,34 @@ __host__ __device__ inline int t_cols(int rank) { return 2 * ((rank + 15) & ~15)
 // [tiles][cap][bn][t_cols].  Entry j of a tile is its j-th distinct adapter in
 // order of first appearance.
 //
-// A CTA takes up to 16 rows of one adapter in one tile as the M side of
-// mma.sync m16n8k16 and the adapter's rank as N; its eight warps split the
-// input columns, 32 at a time, and their sums meet in shared memory in warp
-// order.  Lane t of a quad loads 16 consecutive bytes of a row for both
-// operands, which permutes the columns within a block of 32 alike on both
-// sides.  CTA g also zeroes the rows 16 g .. 16 g + 15 of the tile that are not
-// the adapter's.  Bound by the reads of A and x (each adapter's A once per 16
-// of its rows, from L2 after the first).
+// A cluster of `split` CTAs takes up to 64 rows of one adapter in one tile, each
+// CTA a part of the input columns: 64-column blocks of the rows and of A go
+// through a ring of shared-memory stages (cp.async, 16-byte units swizzled by
+// row), the rows are the M side of mma.sync m16n8k16, the rank the N side, and
+// warps beyond one per 16 rows share a block's columns.  Lane t of a quad takes
+// 16 consecutive bytes of a row for both operands, which permutes the columns
+// of a block alike on both sides.  The warps' sums, then the CTAs' through
+// distributed shared memory, are added in order.  Bound by the reads of A and x
+// (A once per 64 of its rows); the split keeps enough of them in flight when
+// every row has its own adapter.
+constexpr int kShRows = 64;
+constexpr int kShStages = 4;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+    const int n = in ? 16 : 0;   // the rest is filled with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
 template <int NT>   // 8-wide rank blocks
 __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
+    extern __shared__ __align__(128) unsigned char ring[];   // [kShStages][kShRows + 8 NT rows][128 bytes]
     __shared__ __align__(16) int s_id[256];
-    __shared__ int s_rows[16];
-    __shared__ int s_cnt[2];
-    __shared__ float red[8 * 16 * NT * 8 > 8192 ? 8192 : 8 * 16 * NT * 8];
+    __shared__ int s_w[8], s_adapter[256], s_rows[kShRows], s_cnt;
+    constexpr int kStageRows = kShRows + 8 * NT;
     griddep_launch();   // the projection may start on W; it waits for this grid before it reads t
+    cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = blockIdx.x, tile = blockIdx.z;
+    const int part = blockIdx.x % a.split, g = blockIdx.x / a.split, tile = blockIdx.z;
     const int row0 = tile * a.bn, rows = min(a.bn, a.n - row0);
     const int KT = t_cols(a.rank), R16 = KT / 2;
 
@@ -87,7 +98,6 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
             if (v.x == id || (k + 1 < tid && v.y == id) || (k + 2 < tid && v.z == id) || (k + 3 < tid && v.w == id)) first = 0;
         }
     }
-    __shared__ int s_w[8], s_adapter[256];
     const uint32_t fb = __ballot_sync(0xffffffffu, first);
     if (lane == 0) s_w[warp] = __popc(fb);
     __syncthreads();
@@ -98,92 +108,139 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
     }
     if (first) s_adapter[at] = s_id[tid];
     __syncthreads();
-    if (g == 0 && blockIdx.y == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
         if (tid == 0) a.counts[tile] = count;
         if (tid < count) a.entry[tile * a.cap + tid] = s_adapter[tid];
     }
 
+    const int nblk = (a.fin + kPK - 1) / kPK;
+    const int b0 = nblk * part / a.split, nb = nblk * (part + 1) / a.split - b0;   // this CTA's column blocks
     for (int j = blockIdx.y; j < count; j += gridDim.y) {
         const int ad = s_adapter[j];
         __nv_bfloat16* T = a.t + ((size_t)tile * a.cap + j) * a.bn * KT;
-        // zero the other rows of this CTA's sixteen
-        for (int i = tid; i < 16 * (KT / 8); i += 256) {
-            const int rr = 16 * g + i / (KT / 8);
-            if (s_id[rr] != ad) reinterpret_cast<uint4*>(T + (size_t)rr * KT)[i % (KT / 8)] = make_uint4(0, 0, 0, 0);
+        // zero the other rows of the tile's 64 g .. (the CTAs of the cluster in turn)
+        for (int i = tid; i < (kShRows / a.split) * (KT / 8); i += 256) {
+            const int rr = kShRows * g + i / (KT / 8) * a.split + part;
+            if (rr < a.bn && s_id[rr] != ad) reinterpret_cast<uint4*>(T + (size_t)rr * KT)[i % (KT / 8)] = make_uint4(0, 0, 0, 0);
         }
-        // rows 16 g .. of the adapter's, in order
+        // the adapter's rows 64 g .. in order
         if (warp == 0) {
             int seen = 0;
             for (int k0 = 0; k0 < a.bn; k0 += 32) {
                 const bool mine = k0 + lane < a.bn && s_id[k0 + lane] == ad;
                 const uint32_t b = __ballot_sync(0xffffffffu, mine);
-                const int p = seen + __popc(b & ((1u << lane) - 1u)) - 16 * g;
-                if (mine && p >= 0 && p < 16) s_rows[p] = k0 + lane;
+                const int p = seen + __popc(b & ((1u << lane) - 1u)) - kShRows * g;
+                if (mine && p >= 0 && p < kShRows) s_rows[p] = k0 + lane;
                 seen += __popc(b);
             }
-            if (lane == 0) s_cnt[0] = max(0, min(16, seen - 16 * g));
+            if (lane == 0) s_cnt = max(0, min(kShRows, seen - kShRows * g));
         }
         __syncthreads();
-        const int m = s_cnt[0];
-        if (m > 0) {
-            const int gq = lane >> 2, tq = lane & 3;
-            const __nv_bfloat16* xa = a.x + (size_t)(row0 + s_rows[gq < m ? gq : 0]) * a.fin;
-            const __nv_bfloat16* xb = a.x + (size_t)(row0 + s_rows[gq + 8 < m ? gq + 8 : 0]) * a.fin;
-            const bool la = gq < m, lb = gq + 8 < m;
+        const int m = s_cnt;
+        if (m > 0) {   // the same in every CTA of the cluster
             const __nv_bfloat16* A = a.A + (size_t)ad * a.rank * a.fin;
+            auto load = [&](int b) {
+                if (b < nb) {
+                    const uint32_t base = smem_addr(ring) + (b % kShStages) * kStageRows * 128;
+                    for (int i = tid; i < kStageRows * 8; i += 256) {
+                        const int rr = i >> 3, c = i & 7, col = (b0 + b) * kPK + c * 8;
+                        const bool is_x = rr < kShRows;
+                        if (is_x ? rr >= m : rr - kShRows >= R16) continue;   // rows whose products nobody reads
+                        const bool in = col < a.fin && (is_x || rr - kShRows < a.rank);
+                        const __nv_bfloat16* src = is_x ? a.x + (size_t)(row0 + s_rows[rr]) * a.fin + col
+                                                        : A + (size_t)(rr - kShRows) * a.fin + col;
+                        cp_async16(base + rr * 128 + ((c ^ (rr & 7)) << 4), in ? src : a.x, in);
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            const int rtiles = m <= 16 ? 1 : m <= 32 ? 2 : 4, kways = 8 / rtiles;
+            const int rt = warp % rtiles, kidx = warp / rtiles, gq = lane >> 2, tq = lane & 3;
             float acc[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-            const int nblk = (a.fin + 31) / 32;
-#pragma unroll 2
-            for (int b = warp; b < nblk; b += 8) {
-                const int c = b * 32 + tq * 8;
-                const bool in = c < a.fin;
-                const uint4 z = make_uint4(0, 0, 0, 0);
-                const uint4 x0 = in && la ? __ldg(reinterpret_cast<const uint4*>(xa + c)) : z;
-                const uint4 x1 = in && lb ? __ldg(reinterpret_cast<const uint4*>(xb + c)) : z;
+            for (int b = 0; b < kShStages - 1; ++b) load(b);
+            for (int b = 0; b < nb; ++b) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kShStages - 2) : "memory");
+                __syncthreads();   // block b has arrived, and block b - 1's stage is free
+                load(b + kShStages - 1);
+                const unsigned char* p = ring + (b % kShStages) * kStageRows * 128;
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const int rr = t * 8 + gq;
-                    const uint4 w = in && rr < a.rank ? __ldg(reinterpret_cast<const uint4*>(A + (size_t)rr * a.fin + c)) : z;
-                    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                        : "+f"(acc[t][0]), "+f"(acc[t][1]), "+f"(acc[t][2]), "+f"(acc[t][3])
-                        : "r"(x0.x), "r"(x1.x), "r"(x0.y), "r"(x1.y), "r"(w.x), "r"(w.y));
-                    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                        : "+f"(acc[t][0]), "+f"(acc[t][1]), "+f"(acc[t][2]), "+f"(acc[t][3])
-                        : "r"(x0.z), "r"(x1.z), "r"(x0.w), "r"(x1.w), "r"(w.z), "r"(w.w));
-                }
-            }
-            // warp sums through shared memory (at most 8 blocks of the rank at a time)
-            constexpr int PT = NT > 8 ? 8 : NT;
-            const float scale = a.scale[ad];
+                for (int h = 0; h < 2; ++h) {
+                    if ((2 * b + h) % kways != kidx || 16 * rt >= m) continue;
+                    auto unit = [&](int row) {
+                        return *reinterpret_cast<const uint4*>(p + row * 128 + (((tq + 4 * h) ^ (row & 7)) << 4));
+                    };
+                    const uint4 x0 = unit(16 * rt + gq), x1 = unit(16 * rt + 8 + gq);
 #pragma unroll
-            for (int t0 = 0; t0 < NT; t0 += PT) {
-                if (t0) __syncthreads();
-#pragma unroll
-                for (int t = 0; t < PT; ++t) {
-                    float* d = red + ((warp * 16 + gq) * PT + t) * 8 + 2 * tq;
-                    d[0] = acc[t0 + t][0], d[1] = acc[t0 + t][1];
-                    d[8 * PT * 8] = acc[t0 + t][2], d[8 * PT * 8 + 1] = acc[t0 + t][3];
-                }
-                __syncthreads();
-                for (int i = tid; i < m * PT * 8; i += 256) {
-                    const int rr = i / (PT * 8), c = t0 * 8 + i % (PT * 8);
-                    float v = 0.f;
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) v += red[(w * 16 + rr) * PT * 8 + i % (PT * 8)];
-                    if (c < R16) {
-                        v *= scale;   // zero beyond the rank: A's rows there were read as zero
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                        __nv_bfloat16* d = T + (size_t)s_rows[rr] * KT + c;
-                        d[0] = hi;
-                        d[R16] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                    for (int t = 0; t < NT; ++t) {
+                        const uint4 w = unit(kShRows + 8 * t + gq);
+                        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                            : "+f"(acc[t][0]), "+f"(acc[t][1]), "+f"(acc[t][2]), "+f"(acc[t][3])
+                            : "r"(x0.x), "r"(x1.x), "r"(x0.y), "r"(x1.y), "r"(w.x), "r"(w.y));
+                        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                            : "+f"(acc[t][0]), "+f"(acc[t][1]), "+f"(acc[t][2]), "+f"(acc[t][3])
+                            : "r"(x0.z), "r"(x1.z), "r"(x0.w), "r"(x1.w), "r"(w.z), "r"(w.w));
                     }
                 }
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncthreads();
+            // warps' sums, then CTAs', in order
+            float* red = reinterpret_cast<float*>(ring);            // [8][16][8 NT]
+            float* sum = red + 8 * 16 * 8 * NT;                     // [64][8 NT]
+            constexpr int RW = 8 * NT;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float* d = red + (warp * 16 + gq) * RW + 8 * t + 2 * tq;
+                d[0] = acc[t][0], d[1] = acc[t][1];
+                d[8 * RW] = acc[t][2], d[8 * RW + 1] = acc[t][3];
+            }
+            __syncthreads();
+            for (int i = tid; i < m * RW; i += 256) {
+                const int rr = i / RW, c = i % RW;
+                float v = 0.f;
+                for (int k = 0; k < kways; ++k) v += red[((k * rtiles + (rr >> 4)) * 16 + (rr & 15)) * RW + c];
+                sum[i] = v;
+            }
+            if (a.split > 1) cl.sync();
+            else __syncthreads();
+            const float scale = a.scale[ad];
+            const int mine = (m - part + a.split - 1) / a.split;   // rows part, part + split, ..
+            for (int i = tid; i < mine * R16; i += 256) {
+                const int rr = i / R16 * a.split + part, c = i % R16;
+                float v = 0.f;
+                for (int p = 0; p < a.split; ++p) v += cl.map_shared_rank(sum, p)[rr * RW + c];
+                v *= scale;   // zero beyond the rank: A's rows there were filled with zeros
+                const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                __nv_bfloat16* d = T + (size_t)s_rows[rr] * KT + c;
+                d[0] = hi;
+                d[R16] = __float2bfloat16_rn(v - __bfloat162float(hi));
+            }
+            if (a.split > 1) cl.sync();   // the peers have read this CTA's sums
         }
-        __syncthreads();   // red and s_rows are reused
+        __syncthreads();   // the ring and s_rows are reused
     }
+}
+
+template <int NT>
+static cudaError_t shrink_launch(const ShrinkArgs& s, dim3 grid, cudaStream_t st) {
+    const int ring = kShStages * (kShRows + 8 * NT) * 128, sums = (8 * 16 + kShRows) * 8 * NT * 4;
+    const int smem = ring > sums ? ring : sums;
+    cudaError_t e = cudaFuncSetAttribute(k_adapter_shrink<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)s.split;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_adapter_shrink<NT>, s);
 }
 
 // One warp's share of a tile to out: this lane's output feature o (TMEM lane),
@@ -745,16 +802,17 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     if (p.counts) {
         s.bn = p.bn;
         s.cap = p.cap;
-        const int groups = (p.bn + 15) / 16;
+        // CTAs per 64 rows: each at least four column blocks; eight when one tile's adapters leave SMs idle
+        s.split = 1;
+        const int most = s.n <= 16 ? 8 : 4;
+        while (s.split < most && p.kblocks >= 8 * s.split) s.split *= 2;
+        const int groups = (p.bn + kShRows - 1) / kShRows;
         int y = p.cap;
-        while (y > 1 && (int64_t)groups * y * p.row_tiles > 4096) y = (y + 1) / 2;
-        const dim3 grid(groups, y, p.row_tiles);
+        while (y > 1 && (int64_t)groups * s.split * y * p.row_tiles > 4096) y = (y + 1) / 2;
+        const dim3 grid(groups * s.split, y, p.row_tiles);
         const int nt = (p.rank + 7) / 8;
-        if (nt <= 2) k_adapter_shrink<2><<<grid, 256, 0, st>>>(s);
-        else if (nt <= 4) k_adapter_shrink<4><<<grid, 256, 0, st>>>(s);
-        else if (nt <= 8) k_adapter_shrink<8><<<grid, 256, 0, st>>>(s);
-        else k_adapter_shrink<16><<<grid, 256, 0, st>>>(s);
-        e = cudaGetLastError();
+        e = nt <= 2 ? shrink_launch<2>(s, grid, st) : nt <= 4 ? shrink_launch<4>(s, grid, st)
+            : nt <= 8 ? shrink_launch<8>(s, grid, st) : shrink_launch<16>(s, grid, st);
         if (e != cudaSuccess) return e;
     }
     const auto kernel = wk.pair ? k_project_pair : k_project;
