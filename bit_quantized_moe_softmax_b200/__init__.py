@@ -100,7 +100,7 @@ def lib() -> ctypes.CDLL:
                                     vp], i32),
             "ds4moe_widen_rows": ([vp, i32, vp, i32, i32, i32, vp, i32, vp], i32),
             "ds4moe_project": ([vp, i32, vp, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp], i32),
-            "ds4moe_project_work_bytes": ([i32, i32, i32, i32], sz),
+            "ds4moe_project_work_bytes": ([i32, i32, i32, i32, i32], sz),
             "ds4moe_get_project_error": ([vp, ctypes.POINTER(i32)], i32),
             "ds4moe_sample": ([vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
         }
@@ -390,8 +390,8 @@ def ds4moe_widen_rows(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, g
           out.data_ptr(), _ACT[out.dtype])
 
 
-def ds4moe_project_work_bytes(n: int, out_features: int, n_adapters: int, rank: int) -> int:
-    return lib().ds4moe_project_work_bytes(n, out_features, n_adapters, rank)
+def ds4moe_project_work_bytes(n: int, in_features: int, out_features: int, n_adapters: int, rank: int) -> int:
+    return lib().ds4moe_project_work_bytes(n, in_features, out_features, n_adapters, rank)
 
 
 def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch.Tensor | None = None,
@@ -423,7 +423,8 @@ def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch
                                ("ids", ids, (n,), (torch.int32,))))
     if na and n:
         if work is None:
-            work = torch.empty(lib().ds4moe_project_work_bytes(n, fout, na, rank), dtype=torch.uint8, device=x.device)
+            work = torch.empty(lib().ds4moe_project_work_bytes(n, fin, fout, na, rank), dtype=torch.uint8,
+                               device=x.device)
         elif work.get_device() != dev or not work.is_contiguous():
             _refuse(where, "work: contiguous on %s expected" % x.device)
         wb = work.numel() * work.element_size()

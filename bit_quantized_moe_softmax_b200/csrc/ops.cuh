@@ -70,11 +70,12 @@ struct ProjectArgs {
     int bn, row_tiles, cap, kblocks, tiles, split, stages;   // set by the launcher
 };
 struct ProjectWork {            // layout of the caller's work buffer
-    bool pair;
-    int bn, row_tiles, cap;
+    bool pair;                  // CTA pairs of 512 output features per tile; else 128
+    int split;                  // CTAs that share a tile
+    int bn, row_tiles, cap;     // rows per tile, tiles along the rows, entries per tile
     size_t off_entry, off_t, total;
 };
-ProjectWork project_work(int n, int fout, int n_adapters, int rank);
+ProjectWork project_work(int n, int fin, int fout, int n_adapters, int rank);
 cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, const void* W, const void* B, int n_sm,
                            cudaStream_t st);
 cudaError_t read_project_error(uint32_t* code, cudaStream_t st);

@@ -140,9 +140,10 @@ static ds4moe_status check_project(int32_t n, int32_t fin, int32_t fout, int32_t
     return DS4MOE_OK;
 }
 
-size_t ds4moe_project_work_bytes(int32_t n, int32_t out_features, int32_t n_adapters, int32_t rank) {
-    if (n_adapters < 1 || n < 1 || check_project(n, 8, out_features, n_adapters, rank) != DS4MOE_OK) return 0;
-    return project_work(n, out_features, n_adapters, rank).total;
+size_t ds4moe_project_work_bytes(int32_t n, int32_t in_features, int32_t out_features, int32_t n_adapters, int32_t rank) {
+    if (n_adapters < 1 || n < 1 || check_project(n, in_features, out_features, n_adapters, rank) != DS4MOE_OK)
+        return 0;
+    return project_work(n, in_features, out_features, n_adapters, rank).total;
 }
 
 ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_t in_features, int32_t out_features,
@@ -158,7 +159,7 @@ ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_
         return fail(DS4MOE_ERR_ALIGN, "project: x, W, A, B and out must be 16-byte aligned");
     if (ad && (!aligned(d_work, 256) || !aligned(d_scale, 4) || !aligned(d_ids, 4)))
         return fail(DS4MOE_ERR_ALIGN, "project: work must be 256-byte aligned, scale and ids 4-byte");
-    ProjectWork wk = project_work(n, out_features, ad ? n_adapters : 0, ad ? rank : 0);
+    ProjectWork wk = project_work(n, in_features, out_features, ad ? n_adapters : 0, ad ? rank : 0);
     if (ad && work_bytes < wk.total) return fail(DS4MOE_ERR_ARG, "project: work %zu bytes < %zu", work_bytes, wk.total);
     const size_t fi = in_features, fo = out_features, na = n_adapters, r = rank;
     const Span out{d_out, (size_t)n * fo * 2}, work{ad ? d_work : nullptr, wk.total};

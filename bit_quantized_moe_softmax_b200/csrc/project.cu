@@ -74,54 +74,75 @@ template <int NT>   // 8-wide rank blocks
 __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
     extern __shared__ __align__(128) unsigned char ring[];   // [kShStages][kShRows + 8 NT rows][128 bytes]
     __shared__ __align__(16) int s_id[256];
-    __shared__ int s_w[8], s_adapter[256], s_rows[kShRows], s_cnt;
+    __shared__ int s_w[8], s_rank[256], s_adapter[256], s_n[256], s_rows[kShRows], s_j, s_c0, s_cnt;
     constexpr int kStageRows = kShRows + 8 * NT;
     griddep_launch();   // the projection may start on W; it waits for this grid before it reads t
     cg::cluster_group cl = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int part = blockIdx.x % a.split, g = blockIdx.x / a.split, tile = blockIdx.z;
+    const int part = blockIdx.x, tile = blockIdx.z;
     const int row0 = tile * a.bn, rows = min(a.bn, a.n - row0);
     const int KT = t_cols(a.rank), R16 = KT / 2;
 
-    // entry index of each distinct adapter: rank of its first appearance
-    {
-        const int id = tid < rows ? a.ids[row0 + tid] : -1;
-        s_id[tid] = (unsigned)id < (unsigned)a.n_adapters ? id : -1;   // any other id: no adapter
-    }
+    // the tile's distinct adapters in order of first appearance, and how many rows each has
+    const int row_id = tid < rows ? a.ids[row0 + tid] : -1;
+    const int id = (unsigned)row_id < (unsigned)a.n_adapters ? row_id : -1;   // any other id: no adapter
+    s_id[tid] = id;
+    s_n[tid] = 0;
     __syncthreads();
-    int first = 0;
-    if (s_id[tid] >= 0) {
-        const int id = s_id[tid];
-        first = 1;
+    int lead = tid;   // the first row with this id
+    if (id >= 0) {
         for (int k = 0; k < tid; k += 4) {
             const int4 v = *reinterpret_cast<const int4*>(s_id + k);
-            if (v.x == id || (k + 1 < tid && v.y == id) || (k + 2 < tid && v.z == id) || (k + 3 < tid && v.w == id)) first = 0;
+            const int f = v.x == id ? k : v.y == id ? k + 1 : v.z == id ? k + 2 : v.w == id ? k + 3 : 256;
+            lead = min(lead, f);
         }
     }
-    const uint32_t fb = __ballot_sync(0xffffffffu, first);
-    if (lane == 0) s_w[warp] = __popc(fb);
+    auto scan = [&](int v, int& before) {   // exclusive prefix over the threads, and the total
+        int inc = v;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, m);
+            if (lane >= m) inc += o;
+        }
+        __syncthreads();
+        if (lane == 31) s_w[warp] = inc;
+        __syncthreads();
+        int base = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) base += s_w[w];
+            all += s_w[w];
+        }
+        before = base + inc - v;
+        return all;
+    };
+    int at;
+    const int count = scan(id >= 0 && lead == tid, at);
+    if (id >= 0 && lead == tid) s_rank[tid] = at, s_adapter[at] = id;
     __syncthreads();
-    int at = __popc(fb & ((1u << lane) - 1u)), count = 0;
-    for (int w = 0; w < 8; ++w) {
-        if (w < warp) at += s_w[w];
-        count += s_w[w];
-    }
-    if (first) s_adapter[at] = s_id[tid];
+    if (id >= 0) atomicAdd(&s_n[s_rank[lead]], 1);
     __syncthreads();
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         if (tid == 0) a.counts[tile] = count;
         if (tid < count) a.entry[tile * a.cap + tid] = s_adapter[tid];
     }
+    const int chunks = tid < count ? (s_n[tid] + kShRows - 1) / kShRows : 0;
+    int c0;
+    const int items = scan(chunks, c0);   // (adapter, 64 of its rows), shared out among the clusters of this tile
 
     const int nblk = (a.fin + kPK - 1) / kPK;
     const int b0 = nblk * part / a.split, nb = nblk * (part + 1) / a.split - b0;   // this CTA's column blocks
-    for (int j = blockIdx.y; j < count; j += gridDim.y) {
-        const int ad = s_adapter[j];
+    for (int item = blockIdx.y; item < items; item += gridDim.y) {
+        if (c0 <= item && item < c0 + chunks) s_j = tid, s_c0 = c0;   // one thread
+        __syncthreads();
+        const int j = s_j, g = item - s_c0, ad = s_adapter[j];
         __nv_bfloat16* T = a.t + ((size_t)tile * a.cap + j) * a.bn * KT;
-        // zero the other rows of the tile's 64 g .. (the CTAs of the cluster in turn)
-        for (int i = tid; i < (kShRows / a.split) * (KT / 8); i += 256) {
-            const int rr = kShRows * g + i / (KT / 8) * a.split + part;
-            if (rr < a.bn && s_id[rr] != ad) reinterpret_cast<uint4*>(T + (size_t)rr * KT)[i % (KT / 8)] = make_uint4(0, 0, 0, 0);
+        if (g == 0) {   // zero the rows that are not the adapter's (the CTAs of the cluster in turn)
+            const int per = KT / 8;
+            for (int i = tid; i < (a.bn + a.split - 1) / a.split * per; i += 256) {
+                const int rr = i / per * a.split + part;
+                if (rr < a.bn && s_id[rr] != ad) reinterpret_cast<uint4*>(T + (size_t)rr * KT)[i % per] = make_uint4(0, 0, 0, 0);
+            }
         }
         // the adapter's rows 64 g .. in order
         if (warp == 0) {
@@ -133,23 +154,36 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
                 if (mine && p >= 0 && p < kShRows) s_rows[p] = k0 + lane;
                 seen += __popc(b);
             }
-            if (lane == 0) s_cnt = max(0, min(kShRows, seen - kShRows * g));
+            if (lane == 0) s_cnt = min(kShRows, seen - kShRows * g);
         }
         __syncthreads();
         const int m = s_cnt;
-        if (m > 0) {   // the same in every CTA of the cluster
+        {
             const __nv_bfloat16* A = a.A + (size_t)ad * a.rank * a.fin;
+            // this thread's 16-byte units of a stage: column unit tid % 8 of rows tid / 8, tid / 8 + 32, ..
+            constexpr int U = (kStageRows + 31) / 32;
+            const __nv_bfloat16* src[U];
+            uint32_t use = 0;   // bit 2 u: unit u is loaded; bit 2 u + 1: from memory (else zeros)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int rr = (tid >> 3) + 32 * u, col = b0 * kPK + (tid & 7) * 8;
+                const bool is_x = rr < kShRows;
+                // rows whose products nobody reads are left as they are
+                const bool any = is_x ? rr < m : rr - kShRows < R16 && rr < kStageRows;
+                const bool real = any && (is_x || rr - kShRows < a.rank);
+                src[u] = !real ? a.x : is_x ? a.x + (size_t)(row0 + s_rows[rr]) * a.fin + col
+                                            : A + (size_t)(rr - kShRows) * a.fin + col;
+                use |= (uint32_t)any << (2 * u) | (uint32_t)real << (2 * u + 1);
+            }
+            const uint32_t dst0 = smem_addr(ring) + (tid >> 3) * 128 + (((tid & 7) ^ (tid >> 3 & 7)) << 4);
             auto load = [&](int b) {
                 if (b < nb) {
-                    const uint32_t base = smem_addr(ring) + (b % kShStages) * kStageRows * 128;
-                    for (int i = tid; i < kStageRows * 8; i += 256) {
-                        const int rr = i >> 3, c = i & 7, col = (b0 + b) * kPK + c * 8;
-                        const bool is_x = rr < kShRows;
-                        if (is_x ? rr >= m : rr - kShRows >= R16) continue;   // rows whose products nobody reads
-                        const bool in = col < a.fin && (is_x || rr - kShRows < a.rank);
-                        const __nv_bfloat16* src = is_x ? a.x + (size_t)(row0 + s_rows[rr]) * a.fin + col
-                                                        : A + (size_t)(rr - kShRows) * a.fin + col;
-                        cp_async16(base + rr * 128 + ((c ^ (rr & 7)) << 4), in ? src : a.x, in);
+                    const uint32_t dst = dst0 + (b % kShStages) * kStageRows * 128;
+                    const bool in = (b0 + b) * kPK + (tid & 7) * 8 < a.fin;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const bool real = in && (use >> (2 * u + 1) & 1u);
+                        if (use >> (2 * u) & 1u) cp_async16(dst + u * 32 * 128, real ? src[u] + b * kPK : a.x, real);
                     }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
@@ -207,15 +241,18 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
             else __syncthreads();
             const float scale = a.scale[ad];
             const int mine = (m - part + a.split - 1) / a.split;   // rows part, part + split, ..
-            for (int i = tid; i < mine * R16; i += 256) {
-                const int rr = i / R16 * a.split + part, c = i % R16;
-                float v = 0.f;
-                for (int p = 0; p < a.split; ++p) v += cl.map_shared_rank(sum, p)[rr * RW + c];
-                v *= scale;   // zero beyond the rank: A's rows there were filled with zeros
-                const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                __nv_bfloat16* d = T + (size_t)s_rows[rr] * KT + c;
+            for (int i = tid; i < mine * (R16 / 2); i += 256) {
+                const int rr = i / (R16 / 2) * a.split + part, c = 2 * (i % (R16 / 2));
+                float2 v = make_float2(0.f, 0.f);
+                for (int p = 0; p < a.split; ++p) {
+                    const float2 o = *reinterpret_cast<const float2*>(cl.map_shared_rank(sum, p) + rr * RW + c);
+                    v.x += o.x, v.y += o.y;
+                }
+                v.x *= scale, v.y *= scale;   // zero beyond the rank: A's rows there were filled with zeros
+                const uint32_t hi = pack_bf16x2(v.x, v.y);
+                uint32_t* d = reinterpret_cast<uint32_t*>(T + (size_t)s_rows[rr] * KT + c);
                 d[0] = hi;
-                d[R16] = __float2bfloat16_rn(v - __bfloat162float(hi));
+                d[R16 / 2] = pack_bf16x2(v.x - __uint_as_float(hi << 16), v.y - __uint_as_float(hi & 0xffff0000u));
             }
             if (a.split > 1) cl.sync();   // the peers have read this CTA's sums
         }
@@ -739,34 +776,36 @@ static cudaError_t encode(CUtensorMap* map, const void* base, uint64_t cols, uin
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Rows per tile (the N side of an MMA: a multiple of 16, up to 256), and
-// whether CTA pairs take 512 output features of them.  Up to 128 rows: one
-// tile, as narrow as they allow.  More: what ends first when each round of
-// tiles takes the time that the L2 needs to bring its operands, in proportion
-// to the features and rows that an SM loads (128 + bn alone, 256 + bn / 2 in a
-// pair; 64 more for a round's start and end).  4096 x 4096 x 4096: pairs of 240
-// rows, two rounds, against four of 256 x 128.
-static bool project_tile(int n, int fout, int& bn) {
+// Rows per tile (the N side of an MMA: a multiple of 16, up to 256), whether
+// CTA pairs take 512 output features of them, and how many CTAs share a tile:
+// what should end first.  A K block takes an SM the time in which the L2 brings
+// its operands, 33 bytes a clock with all SMs reading (128 bytes per feature
+// and row; the MMAs take less at every size here); a round of tiles some more
+// clocks for its start and end, above all the pairs' epilogue.
+// 4096 x 4096 x 4096: pairs of 240 rows, two rounds, 101 us; single CTAs 174 us.
+// 500 x 2056 x 5001: single CTAs of 176 rows, 26 us; pairs of 80 rows 31 us.
+static void project_tile(int n, int fin, int fout, ProjectWork& w) {
     constexpr int64_t n_sm = 148;   // the size of the work buffer must not depend on the current device
-    if (n <= 128) {
-        bn = (n + 15) & ~15;
-        return false;
-    }
-    bool pair = false;
+    const int64_t kb = (fin + kPK - 1) / kPK;
     int64_t cost = INT64_MAX;
-    for (int b = 256; b >= 64; b -= 16) {
-        const int64_t rows = (n + b - 1) / b;
-        const int64_t alone = (rows * ((fout + kPM - 1) / kPM) + n_sm - 1) / n_sm * (128 + b + 64);
-        const int64_t both = (rows * ((fout + 4 * kPM - 1) / (4 * kPM)) + n_sm / 2 - 1) / (n_sm / 2) * (256 + b / 2 + 64);
-        if (alone < cost) cost = alone, bn = b, pair = false;
-        if (both < cost) cost = both, bn = b, pair = true;
+    const int widest = n <= 256 ? (n + 15) & ~15 : 256;
+    for (int b = widest; b >= 16 && (b == widest || b >= 64); b -= 16) {
+        const int64_t rows = (n + b - 1) / b, alone = rows * ((fout + kPM - 1) / kPM);
+        for (int64_t split = 1; split <= 8; split *= 2) {
+            if (split > 1 && (alone * split > n_sm || kb < 4 * split)) break;
+            const int64_t rounds = (alone + n_sm - 1) / n_sm;
+            const int64_t c = rounds * ((kb + split - 1) / split * (kPM + b) * 128 / 33 + 5000) + (split > 1 ? 3000 + b * 8 : 0);
+            if (c < cost) cost = c, w.bn = b, w.pair = false, w.split = (int)split;
+        }
+        const int64_t both = rows * ((fout + 4 * kPM - 1) / (4 * kPM)), rounds = (both + n_sm / 2 - 1) / (n_sm / 2);
+        const int64_t c = rounds * (kb * (2 * kPM + b / 2) * 128 / 33 + 8000 + b * 17);
+        if (c < cost) cost = c, w.bn = b, w.pair = true, w.split = 1;
     }
-    return pair;
 }
 
-ProjectWork project_work(int n, int fout, int n_adapters, int rank) {
+ProjectWork project_work(int n, int fin, int fout, int n_adapters, int rank) {
     ProjectWork w{};
-    w.pair = project_tile(n, fout, w.bn);
+    project_tile(n, fin, fout, w);
     w.row_tiles = (n + w.bn - 1) / w.bn;
     w.cap = n_adapters < w.bn ? n_adapters : w.bn;
     auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
@@ -784,9 +823,7 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     p.kblocks = (p.fin + kPK - 1) / kPK;
     const int features = wk.pair ? 4 * kPM : kPM;
     p.tiles = (p.fout + features - 1) / features * p.row_tiles;
-    // Few tiles: several CTAs share one, as many as leave each four blocks of W and find an SM of their own.
-    p.split = 1;
-    while (!wk.pair && p.split < 8 && (int64_t)p.tiles * p.split * 2 <= n_sm && p.kblocks >= p.split * 2 * 4) p.split *= 2;
+    p.split = wk.split;
     const int stage = wk.pair ? 2 * kPStageA + p.bn / 2 * kPK * 2 : kPStageA + p.bn * kPK * 2;
     p.stages = kPSmem / stage < kPMaxStages ? kPSmem / stage : kPMaxStages;
     const int smem = 1024 + p.stages * stage;   // the partial sums of a split tile (512 bytes per row) fit as well
@@ -802,14 +839,14 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     if (p.counts) {
         s.bn = p.bn;
         s.cap = p.cap;
-        // CTAs per 64 rows: each at least four column blocks; eight when one tile's adapters leave SMs idle
+        // CTAs per item: each at least four column blocks; eight for a few rows, which leave SMs idle
         s.split = 1;
         const int most = s.n <= 16 ? 8 : 4;
         while (s.split < most && p.kblocks >= 8 * s.split) s.split *= 2;
-        const int groups = (p.bn + kShRows - 1) / kShRows;
-        int y = p.cap;
-        while (y > 1 && (int64_t)groups * s.split * y * p.row_tiles > 4096) y = (y + 1) / 2;
-        const dim3 grid(groups * s.split, y, p.row_tiles);
+        // clusters per tile: as many as it can have items, or as fill the SMs about four times over
+        const int items = p.cap + p.bn / kShRows, fill = 4 * n_sm / (s.split * p.row_tiles);
+        const int y = items < fill ? items : fill < 4 ? 4 : fill;
+        const dim3 grid(s.split, y, p.row_tiles);
         const int nt = (p.rank + 7) / 8;
         e = nt <= 2 ? shrink_launch<2>(s, grid, st) : nt <= 4 ? shrink_launch<4>(s, grid, st)
             : nt <= 8 ? shrink_launch<8>(s, grid, st) : shrink_launch<16>(s, grid, st);

@@ -273,7 +273,8 @@ ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_
 
 /* Bytes of scratch a ds4moe_project of n rows needs (0 without adapters, and
  * for sizes that it refuses): about n * min(256, n_adapters) * rank * 4. */
-size_t ds4moe_project_work_bytes(int32_t n, int32_t out_features, int32_t n_adapters, int32_t rank);
+size_t ds4moe_project_work_bytes(int32_t n, int32_t in_features, int32_t out_features, int32_t n_adapters,
+                                 int32_t rank);
 
 /* Synchronize `stream`, then read and clear the current device's error word of
  * ds4moe_project into *code (0 = none, bit 1 = a bounded wait timed out, with
