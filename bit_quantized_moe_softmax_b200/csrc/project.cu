@@ -30,6 +30,7 @@ constexpr int kPK = 64;                  // K columns per block (one 128-byte sw
 constexpr int kPStageA = kPM * kPK * 2;
 constexpr int kPThreads = 256;           // warps: 0 TMA, 1 MMA, 2 TMEM, 4..7 epilogue
 constexpr int kPMaxStages = 10;
+constexpr int kAhead = 16;
 constexpr int kPSmem = 200 * 1024;       // of 227 KB
 
 // Error word of the projection's bounded waits, one per device.
@@ -40,6 +41,26 @@ struct ProjSmem {
     uint64_t accF[2], accE[2];
     uint32_t tmem;
     volatile uint32_t abort;
+    int ahead[kAhead];
+};
+
+// The adapters of a tile's entries j0, j0 + step, .. for one thread, kAhead
+// loads at a time: one by one each would cost the loop a trip to the L2.
+struct Entries {
+    const int32_t* p;
+    int* buf;
+    int count;
+    __device__ __forceinline__ int get(int j, int first, int step) const {
+        const int i = (j - first) / step % kAhead;
+        if (i == 0) {
+            int v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) v[k] = j + k * step < count ? __ldcg(p + j + k * step) : 0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) buf[k] = v[k];
+        }
+        return buf[i];
+    }
 };
 
 // bf16 columns of one row of t: hi pieces, then lo pieces
@@ -349,6 +370,16 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
         }
         S.abort = 0;
         fence_barrier_init();
+        // the first tile's first blocks are on their way before the others are set up
+        if (first < a.tiles) {
+            const int o0 = first / a.row_tiles * kPM, r0 = first % a.row_tiles * a.bn;
+            for (int i = 0; i < min(a.stages, kb1 - kb0); ++i) {
+                unsigned char* p = st + i * stage_bytes;
+                mbar_arrive_expect_tx(&S.full[i], stage_bytes);
+                tma_load_2d(p, &mapW, (kb0 + i) * kPK, o0, &S.full[i]);
+                tma_load_2d(p + kPStageA, &mapX, (kb0 + i) * kPK, r0, &S.full[i]);
+            }
+        }
     }
     if (warp == 2) {
         tmem_alloc(&S.tmem, acc_cols);
@@ -378,7 +409,9 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
             };
             for (int tile = first; tile < a.tiles && !S.abort; tile += step) {
                 const int o0 = tile / a.row_tiles * kPM, rt = tile % a.row_tiles, r0 = rt * a.bn;
-                for (int kb = kb0; kb < kb1; ++kb) {
+                int kb = kb0;
+                if (tile == first) it = min(a.stages, kb1 - kb0), kb += it;   // sent above
+                for (; kb < kb1; ++kb) {
                     const int s = slot();
                     if (s < 0) break;
                     unsigned char* p = st + s * stage_bytes;
@@ -391,9 +424,9 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
                         asm volatile("fence.proxy.async.global;" ::: "memory");
                         waited = true;
                     }
-                    const int count = __ldcg(a.counts + rt);
-                    for (int j = rank_in; j < count && !S.abort; j += a.split) {
-                        const int ad = __ldcg(a.entry + rt * a.cap + j);
+                    const Entries entries{a.entry + rt * a.cap, S.ahead, __ldcg(a.counts + rt)};
+                    for (int j = rank_in; j < entries.count && !S.abort; j += a.split) {
+                        const int ad = entries.get(j, rank_in, a.split);
                         const int trow = (rt * a.cap + j) * a.bn;
                         for (int b = 0; b < per_entry; ++b) {
                             const int s = slot();
@@ -537,6 +570,7 @@ struct PairSmem {
     uint64_t accF, accE[2];
     uint32_t tmem;
     volatile uint32_t abort;
+    int ahead[kAhead];
 };
 constexpr int kPairThreads = 384;   // warps: 0 TMA, 1 MMA (leader), 2 TMEM, 4..11 epilogue
 
@@ -645,9 +679,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                         asm volatile("fence.proxy.async.global;" ::: "memory");
                         waited = true;
                     }
-                    const int count = __ldcg(a.counts + rt);
-                    for (int j = 0; j < count && !S.abort; ++j) {
-                        const int ad = __ldcg(a.entry + rt * a.cap + j);
+                    const Entries entries{a.entry + rt * a.cap, S.ahead, __ldcg(a.counts + rt)};
+                    for (int j = 0; j < entries.count && !S.abort; ++j) {
+                        const int ad = entries.get(j, 0, 1);
                         const int trow = (rt * a.cap + j) * a.bn + r * half;
                         for (int b = 0; b < per_entry; ++b) {
                             const int s = slot();
