@@ -61,23 +61,28 @@ struct ShrinkArgs {
     int32_t* counts;            // [tiles] distinct adapters of a tile
     int32_t* entry;             // [tiles][cap] their indices
     __nv_bfloat16* t;           // [tiles][cap][bn][2 * rank rounded to 16]
+    float* rows;                // or, for a decode batch, t in binary32 [n][rank] (counts, entry, t: nullptr)
 };
 struct ProjectArgs {
     __nv_bfloat16* out;         // [n][fout]
     int n, fin, fout, rank;
-    const int32_t* counts;      // as above, nullptr without adapters
+    const int32_t* counts;      // as above, nullptr without adapters and for a decode batch
     const int32_t* entry;
+    const float* rows;          // a decode batch's t
+    const __nv_bfloat16* B;     // [n_adapters][fout][rank]
+    const int32_t* ids;         // [n]
+    int n_adapters;
     int bn, row_tiles, cap, kblocks, tiles, split, stages;   // set by the launcher
 };
 struct ProjectWork {            // layout of the caller's work buffer
+    bool rows;                  // a decode batch: the adapters' second product outside the MMAs
     bool pair;                  // CTA pairs of 512 output features per tile; else 128
     int split;                  // CTAs that share a tile
     int bn, row_tiles, cap;     // rows per tile, tiles along the rows, entries per tile
     size_t off_entry, off_t, total;
 };
 ProjectWork project_work(int n, int fin, int fout, int n_adapters, int rank);
-cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, const void* W, const void* B, int n_sm,
-                           cudaStream_t st);
+cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, const void* W, int n_sm, cudaStream_t st);
 cudaError_t read_project_error(uint32_t* code, cudaStream_t st);
 
 }  // namespace ds4

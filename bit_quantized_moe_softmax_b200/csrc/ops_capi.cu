@@ -183,11 +183,18 @@ ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_
         sh.A = (const __nv_bfloat16*)d_A;
         sh.scale = d_scale;
         sh.ids = d_ids;
-        p.counts = sh.counts = (int32_t*)w;
-        p.entry = sh.entry = (int32_t*)(w + wk.off_entry);
-        sh.t = (__nv_bfloat16*)(w + wk.off_t);
+        p.B = (const __nv_bfloat16*)d_B;
+        p.ids = d_ids;
+        p.n_adapters = n_adapters;
+        if (wk.rows) {
+            p.rows = sh.rows = (float*)(w + wk.off_t);
+        } else {
+            p.counts = sh.counts = (int32_t*)w;
+            p.entry = sh.entry = (int32_t*)(w + wk.off_entry);
+            sh.t = (__nv_bfloat16*)(w + wk.off_t);
+        }
     }
-    return done(launch_project(p, sh, wk, d_W, d_B, n_sm, (cudaStream_t)stream), "project launch");
+    return done(launch_project(p, sh, wk, d_W, n_sm, (cudaStream_t)stream), "project launch");
 }
 
 ds4moe_status ds4moe_get_project_error(void* stream, int32_t* code) {

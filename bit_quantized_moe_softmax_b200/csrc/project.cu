@@ -31,7 +31,9 @@ constexpr int kPStageA = kPM * kPK * 2;
 constexpr int kPThreads = 256;           // warps: 0 TMA, 1 MMA, 2 TMEM, 4..7 epilogue
 constexpr int kPMaxStages = 10;
 constexpr int kAhead = 16;
+constexpr int kRowsMin = 8, kRowsMax = 64;   // rows whose adapters the draining warps add
 constexpr int kPSmem = 200 * 1024;       // of 227 KB
+constexpr int kPSmemRows = 168 * 1024;   // beside a CTA of the first kernel
 
 // Error word of the projection's bounded waits, one per device.
 __device__ uint32_t g_project_err;
@@ -42,6 +44,7 @@ struct ProjSmem {
     uint32_t tmem;
     volatile uint32_t abort;
     int ahead[kAhead];
+    int ids[kRowsMax];
 };
 
 // The adapters of a tile's entries j0, j0 + step, .. for one thread, kAhead
@@ -83,7 +86,6 @@ __host__ __device__ inline int t_cols(int rank) { return 2 * ((rank + 15) & ~15)
 // distributed shared memory, are added in order.  Bound by the reads of A and x
 // (A once per 64 of its rows); the split keeps enough of them in flight when
 // every row has its own adapter.
-constexpr int kShRows = 64;
 constexpr int kShStages = 4;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -91,8 +93,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
-template <int NT>   // 8-wide rank blocks
-__global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
+template <int NT, int kShRows>   // 8-wide rank blocks; rows per item
+__global__ void __launch_bounds__(256, NT >= 8 ? 2 : NT == 4 ? 4 : 5) k_adapter_shrink(ShrinkArgs a) {
     extern __shared__ __align__(128) unsigned char ring[];   // [kShStages][kShRows + 8 NT rows][128 bytes]
     __shared__ __align__(16) int s_id[256];
     __shared__ int s_w[8], s_rank[256], s_adapter[256], s_n[256], s_rows[kShRows], s_j, s_c0, s_cnt;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
     __syncthreads();
     if (id >= 0) atomicAdd(&s_n[s_rank[lead]], 1);
     __syncthreads();
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (a.counts && blockIdx.x == 0 && blockIdx.y == 0) {
         if (tid == 0) a.counts[tile] = count;
         if (tid < count) a.entry[tile * a.cap + tid] = s_adapter[tid];
     }
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
         __syncthreads();
         const int j = s_j, g = item - s_c0, ad = s_adapter[j];
         __nv_bfloat16* T = a.t + ((size_t)tile * a.cap + j) * a.bn * KT;
-        if (g == 0) {   // zero the rows that are not the adapter's (the CTAs of the cluster in turn)
+        if (g == 0 && !a.rows) {   // zero the rows that are not the adapter's (the CTAs of the cluster in turn)
             const int per = KT / 8;
             for (int i = tid; i < (a.bn + a.split - 1) / a.split * per; i += 256) {
                 const int rr = i / per * a.split + part;
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            const int rtiles = m <= 16 ? 1 : m <= 32 ? 2 : 4, kways = 8 / rtiles;
+            const int rtiles = kShRows == 16 || m <= 16 ? 1 : m <= 32 ? 2 : 4, kways = 8 / rtiles;
             const int rt = warp % rtiles, kidx = warp / rtiles, gq = lane >> 2, tq = lane & 3;
             float acc[NT][4];
 #pragma unroll
@@ -270,6 +272,10 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
                     v.x += o.x, v.y += o.y;
                 }
                 v.x *= scale, v.y *= scale;   // zero beyond the rank: A's rows there were filled with zeros
+                if (a.rows) {
+                    if (c < a.rank) *reinterpret_cast<float2*>(a.rows + (size_t)(row0 + s_rows[rr]) * a.rank + c) = v;
+                    continue;
+                }
                 const uint32_t hi = pack_bf16x2(v.x, v.y);
                 uint32_t* d = reinterpret_cast<uint32_t*>(T + (size_t)s_rows[rr] * KT + c);
                 d[0] = hi;
@@ -281,11 +287,11 @@ __global__ void __launch_bounds__(256) k_adapter_shrink(ShrinkArgs a) {
     }
 }
 
-template <int NT>
+template <int NT, int kShRows>
 static cudaError_t shrink_launch(const ShrinkArgs& s, dim3 grid, cudaStream_t st) {
     const int ring = kShStages * (kShRows + 8 * NT) * 128, sums = (8 * 16 + kShRows) * 8 * NT * 4;
     const int smem = ring > sums ? ring : sums;
-    cudaError_t e = cudaFuncSetAttribute(k_adapter_shrink<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(k_adapter_shrink<NT, kShRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -298,39 +304,112 @@ static cudaError_t shrink_launch(const ShrinkArgs& s, dim3 grid, cudaStream_t st
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_adapter_shrink<NT>, s);
+    return cudaLaunchKernelEx(&cfg, k_adapter_shrink<NT, kShRows>, s);
 }
 
-// One warp's share of a tile to out: this lane's output feature o (TMEM lane),
-// the rows r0 .. r0 + rows - 1 as columns from taddr on.  Two lanes exchange
-// half of their values, so that a lane stores two features of one row at once.
-// Not ok (a wait ran out): NaN.
-__device__ __forceinline__ void store_tile(const ProjectArgs& a, uint32_t taddr, int o, int lane, int r0, int rows, bool ok) {
+// 8 to 64 rows (a decode batch; fewer are faster by the MMAs: 14 against 20 us for
+// one row at 4096 x 4096): a block of the K axis per adapter would be
+// zero but for a row or two, so the warps that drain the accumulators add the
+// adapters themselves, in binary32, while the MMAs run: a lane has one output
+// feature and reads its `rank` values of B for each row (a warp: consecutive
+// memory), eight rows' loads in flight.  acc[i] += B[id][o] . t for rows
+// lo + i < hi; ts, ids: t [rows][rank] and the rows' adapters (or -1) in shared
+// memory.
+__device__ __forceinline__ void adapter_rows(const ProjectArgs& a, const float* ts, const int* ids, int o, int lo, int hi,
+                                             float (&acc)[kRowsMax]) {
+#pragma unroll
+    for (int i = 0; i < kRowsMax; ++i) acc[i] = 0.f;
+    const __nv_bfloat16* B = a.B + (size_t)(o < a.fout ? o : 0) * a.rank;
+    const size_t stride = (size_t)a.fout * a.rank;
+#pragma unroll
+    for (int c = 0; c < kRowsMax; c += 8) {
+        if (lo + c >= hi) break;
+        for (int k = 0; k < a.rank; k += 8) {
+            uint4 w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int id = lo + c + j < hi ? ids[lo + c + j] : -1;
+                w[j] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(B + (size_t)id * stride + k)) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int row = lo + c + j;
+                if (row < hi && ids[row] >= 0) {
+                    const float4 t0 = *reinterpret_cast<const float4*>(ts + row * a.rank + k);
+                    const float4 t1 = *reinterpret_cast<const float4*>(ts + row * a.rank + k + 4);
+                    const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                    const float t[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[c + j] = fmaf(__uint_as_float(x[e] << 16), t[2 * e], acc[c + j]);
+                        acc[c + j] = fmaf(__uint_as_float(x[e] & 0xffff0000u), t[2 * e + 1], acc[c + j]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// t and the adapters of up to 64 rows into shared memory, by `threads` threads
+// that meet at barrier 1.
+__device__ __forceinline__ void stage_rows(const ProjectArgs& a, float* ts, int* ids, int i0, int threads) {
+    griddep_wait();   // t is the first kernel's
+    for (int i = i0; i < a.n * a.rank / 4; i += threads)
+        reinterpret_cast<float4*>(ts)[i] = __ldcg(reinterpret_cast<const float4*>(a.rows) + i);
+    for (int i = i0; i < a.n; i += threads) {
+        const int id = __ldg(a.ids + i);
+        ids[i] = (unsigned)id < (unsigned)a.n_adapters ? id : -1;
+    }
+    named_sync(1, threads);
+}
+
+// Sixteen rows of one warp's share of a tile to out: v, the binary32 bits of
+// this lane's output feature o (a TMEM lane) in rows r0 .. r0 + rows - 1.  Two
+// lanes exchange half of their values, so that a lane stores two features of
+// one row at once.
+__device__ __forceinline__ void store16(const ProjectArgs& a, const uint32_t (&v)[16], int o, int lane, int r0, int rows) {
     __nv_bfloat16* dst = a.out + (size_t)r0 * a.fout;
-    const bool pairs = (a.fout & 1) == 0;
-    for (int c0 = 0; c0 < rows; c0 += 16) {
+    if ((a.fout & 1) == 0) {
+        const int odd = lane & 1;
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            // an even lane takes row j, an odd one row j + 1
+            const uint32_t mine = odd ? v[j + 1] : v[j], other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const uint32_t w = pack_bf16x2(__uint_as_float(odd ? other : mine), __uint_as_float(odd ? mine : other));
+            if (o < a.fout && j + odd < rows) *reinterpret_cast<uint32_t*>(dst + (size_t)(j + odd) * a.fout + (o & ~1)) = w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (o < a.fout && j < rows) dst[(size_t)j * a.fout + o] = __float2bfloat16_rn(__uint_as_float(v[j]));
+    }
+}
+
+// A tile's accumulators (columns from taddr on) to out, with what the adapters
+// add to up to 64 rows (acc).  Not ok (a wait ran out): NaN.
+template <bool Rows, int N>
+__device__ __forceinline__ void store_tile(const ProjectArgs& a, uint32_t taddr, int o, int lane, int r0, int rows, bool ok,
+                                           const float (&acc)[N]) {
+    auto sixteen = [&](int c0) {
         uint32_t v[16];
         tmem_ld_32x16(taddr + c0, v);
         tmem_wait_ld();
+        if constexpr (Rows) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + acc[c0 + j]);
+        }
         if (!ok) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) v[j] = 0x7fffffffu;
         }
-        if (pairs) {
-            const int odd = lane & 1;
+        store16(a, v, o, lane, r0 + c0, rows - c0);
+    };
+    if constexpr (Rows) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-                // an even lane takes row j, an odd one row j + 1
-                const uint32_t mine = odd ? v[j + 1] : v[j], other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-                const uint32_t w = pack_bf16x2(__uint_as_float(odd ? other : mine), __uint_as_float(odd ? mine : other));
-                if (o < a.fout && c0 + j + odd < rows)
-                    *reinterpret_cast<uint32_t*>(dst + (size_t)(c0 + j + odd) * a.fout + (o & ~1)) = w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (o < a.fout && c0 + j < rows) dst[(size_t)(c0 + j) * a.fout + o] = __float2bfloat16_rn(__uint_as_float(v[j]));
-        }
+        for (int c0 = 0; c0 < kRowsMax; c0 += 16)
+            if (c0 < rows) sixteen(c0);
+    } else {
+        for (int c0 = 0; c0 < rows; c0 += 16) sixteen(c0);
     }
 }
 
@@ -343,7 +422,10 @@ __device__ __forceinline__ void store_tile(const ProjectArgs& a, uint32_t taddr,
 // split > 1 (few tiles): a cluster of CTAs shares one tile, each takes a part
 // of W's columns and every split-th adapter, and the partial sums meet through
 // distributed shared memory in CTA order.
-__global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ CUtensorMap mapW,
+// Rows: a decode batch's adapters by adapter_rows (bounded as if for 512 threads:
+// 128 registers leave a CTA of the first kernel room on the SM).
+template <bool Rows>
+__global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __grid_constant__ CUtensorMap mapW,
                                                        const __grid_constant__ CUtensorMap mapX,
                                                        const __grid_constant__ CUtensorMap mapB,
                                                        const __grid_constant__ CUtensorMap mapT, ProjectArgs a) {
@@ -418,7 +500,7 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
                     tma_load_2d(p, &mapW, kb * kPK, o0, &S.full[s]);
                     tma_load_2d(p + kPStageA, &mapX, kb * kPK, r0, &S.full[s]);
                 }
-                if (a.counts) {
+                if (!Rows && a.counts) {
                     if (!waited) {
                         griddep_wait();
                         asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -477,7 +559,7 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
                     steps(s, kPK / 16, 0);
                     umma_commit(&S.empty[s]);
                 }
-                if (a.counts && !S.abort) {
+                if (!Rows && a.counts && !S.abort) {
                     if (!waited) {
                         griddep_wait();
                         waited = true;
@@ -502,14 +584,20 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
     } else if (warp >= 4) {
         const int qd = warp & 3;   // TMEM lanes 32 qd .. 32 qd + 31
         uint32_t use = 0;
+        float* ts = reinterpret_cast<float*>(st + a.stages * stage_bytes);
+        if constexpr (Rows) stage_rows(a, ts, S.ids, tid - 128, 128);
+        const int per = (a.bn + a.split - 1) / a.split;   // rows that this CTA of a split tile finishes
         for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
             const int buf = use & 1;
-            if (!mbar_wait(&S.accF[buf], (use >> 1) & 1, err)) S.abort = 1;
-            const bool ok = !S.abort;   // a wait that ran out leaves NaN in the tile
-            tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + buf * a.bn;
             const int o = tile / a.row_tiles * kPM + 32 * qd + lane, r0 = tile % a.row_tiles * a.bn;
             const int rows = min(a.bn, a.n - r0);
+            float acc[Rows ? kRowsMax : 1];
+            const int lo = per * rank_in;
+            if constexpr (Rows) adapter_rows(a, ts, S.ids, o, lo, min(rows, lo + per), acc);
+            if (!mbar_wait(&S.accF[buf], (use >> 1) & 1, err)) S.abort = 1;
+            const bool ok = !S.abort;   // a wait that ran out leaves NaN in the tile
+            tc_fence_after();
             if (a.split > 1) {
                 float* part = reinterpret_cast<float*>(st) + 32 * qd + lane;   // [bn][128]; every stage is done with
                 for (int c0 = 0; c0 < a.bn; c0 += 16) {
@@ -519,8 +607,13 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
 #pragma unroll
                     for (int j = 0; j < 16; ++j) part[(c0 + j) * kPM] = ok ? __uint_as_float(v[j]) : __int_as_float(0x7fffffff);
                 }
+                if constexpr (Rows) {
+#pragma unroll
+                    for (int j = 0; j < kRowsMax / 2; ++j)
+                        if (j < per && lo + j < rows) part[(lo + j) * kPM] += acc[j];
+                }
             } else {
-                store_tile(a, taddr, o, lane, r0, rows, ok);
+                store_tile<Rows>(a, taddr, o, lane, r0, rows, ok, acc);
             }
             tc_fence_before();
             __syncwarp();
@@ -547,7 +640,7 @@ __global__ void __launch_bounds__(kPThreads) k_project(const __grid_constant__ C
         }
         cl.sync();   // peers have read this CTA's sums
     }
-    if (a.counts) griddep_wait();   // this grid's end implies the first one's
+    if (Rows || a.counts) griddep_wait();   // this grid's end implies the first one's
     tc_fence_before();
     __syncthreads();
     if (warp == 2) {
@@ -571,6 +664,7 @@ struct PairSmem {
     uint32_t tmem;
     volatile uint32_t abort;
     int ahead[kAhead];
+    int ids[kRowsMax];
 };
 constexpr int kPairThreads = 384;   // warps: 0 TMA, 1 MMA (leader), 2 TMEM, 4..11 epilogue
 
@@ -609,7 +703,8 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
                  : "memory");
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
+template <bool Rows>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Rows ? 512 : kPairThreads, 1)
     k_project_pair(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
                    const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapT, ProjectArgs a) {
     extern __shared__ unsigned char smem_raw[];
@@ -673,7 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                     pair_load_2d(p + kPStageA, &mapW, kb * kPK, o0 + 2 * kPM, bar);
                     pair_load_2d(p + 2 * kPStageA, &mapX, kb * kPK, r0, bar);
                 }
-                if (a.counts) {
+                if (!Rows && a.counts) {
                     if (!waited) {
                         griddep_wait();
                         asm volatile("fence.proxy.async.global;" ::: "memory");
@@ -737,7 +832,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                     if (!block(kPK / 16, 0, false)) break;
                     next();
                 }
-                if (a.counts && !S.abort) {
+                if (!Rows && a.counts && !S.abort) {
                     if (!waited) {
                         griddep_wait();
                         waited = true;
@@ -759,13 +854,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
     } else if (warp >= 4) {
         const int qd = warp & 3, m = (warp - 4) >> 2;   // TMEM lanes 32 qd .., accumulator m
         uint32_t use = 0;
+        float* ts = reinterpret_cast<float*>(st + a.stages * stage_bytes);
+        if constexpr (Rows) stage_rows(a, ts, S.ids, tid - 128, kPairThreads - 128);
         for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
+            const int o = tile / a.row_tiles * (4 * kPM) + m * (2 * kPM) + r * kPM + 32 * qd + lane, r0 = tile % a.row_tiles * a.bn;
+            const int rows = min(a.bn, a.n - r0);
+            float acc[Rows ? kRowsMax : 1];
+            if constexpr (Rows) adapter_rows(a, ts, S.ids, o, 0, rows, acc);
             if (!mbar_wait(&S.accF, use & 1, err)) stop();
             const bool ok = !S.abort;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + m * a.bn;
-            const int o = tile / a.row_tiles * (4 * kPM) + m * (2 * kPM) + r * kPM + 32 * qd + lane, r0 = tile % a.row_tiles * a.bn;
-            store_tile(a, taddr, o, lane, r0, min(a.bn, a.n - r0), ok);
+            store_tile<Rows>(a, taddr, o, lane, r0, rows, ok, acc);
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
@@ -773,7 +873,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads)
                              : "memory");
         }
     }
-    if (a.counts) griddep_wait();
+    if (Rows || a.counts) griddep_wait();
     __syncwarp();
     tc_fence_before();
     cl.sync();   // neither CTA leaves while the other may still read its operands or signal its barriers
@@ -841,15 +941,17 @@ ProjectWork project_work(int n, int fin, int fout, int n_adapters, int rank) {
     ProjectWork w{};
     project_tile(n, fin, fout, w);
     w.row_tiles = (n + w.bn - 1) / w.bn;
+    w.rows = n >= kRowsMin && n <= kRowsMax;
     w.cap = n_adapters < w.bn ? n_adapters : w.bn;
     auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
     w.off_entry = up((size_t)w.row_tiles * 4);
     w.off_t = w.off_entry + up((size_t)w.row_tiles * w.cap * 4);
     w.total = w.off_t + up((size_t)w.row_tiles * w.cap * w.bn * t_cols(rank) * 2);
+    if (w.rows) w.off_t = 0, w.total = up((size_t)n * rank * 4);
     return w;
 }
 
-cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, const void* W, const void* B, int n_sm,
+cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, const void* W, int n_sm,
                            cudaStream_t st) {
     p.bn = wk.bn;
     p.row_tiles = wk.row_tiles;
@@ -859,18 +961,21 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     p.tiles = (p.fout + features - 1) / features * p.row_tiles;
     p.split = wk.split;
     const int stage = wk.pair ? 2 * kPStageA + p.bn / 2 * kPK * 2 : kPStageA + p.bn * kPK * 2;
-    p.stages = kPSmem / stage < kPMaxStages ? kPSmem / stage : kPMaxStages;
-    const int smem = 1024 + p.stages * stage;   // the partial sums of a split tile (512 bytes per row) fit as well
+    // a decode batch with adapters leaves room for a CTA of the first kernel beside this one, so that W streams
+    // meanwhile (one row at 4096 x 4096: 14 us, without it 19)
+    const int t_bytes = p.rows ? p.n * p.rank * 4 : 0, room = p.rows || (p.counts && p.bn <= kRowsMax) ? kPSmemRows : kPSmem;
+    p.stages = (room - t_bytes) / stage < kPMaxStages ? (room - t_bytes) / stage : kPMaxStages;
+    const int smem = 1024 + p.stages * stage + t_bytes;   // the partial sums of a split tile (512 bytes per row) fit as well
 
     CUtensorMap mW, mX, mB = {}, mT = {};
     cudaError_t e = encode(&mW, W, p.fin, p.fout, 1, 2, kPM);
     if (e == cudaSuccess) e = encode(&mX, s.x, p.fin, p.n, 1, 2, wk.pair ? p.bn / 2 : p.bn);
-    if (e == cudaSuccess && p.counts) e = encode(&mB, B, p.rank, p.fout, s.n_adapters, 3, kPM);
+    if (e == cudaSuccess && p.counts) e = encode(&mB, p.B, p.rank, p.fout, s.n_adapters, 3, kPM);
     if (e == cudaSuccess && p.counts)
         e = encode(&mT, s.t, t_cols(p.rank), (uint64_t)p.row_tiles * p.cap * p.bn, 1, 2, wk.pair ? p.bn / 2 : p.bn);
     if (e != cudaSuccess) return e;
 
-    if (p.counts) {
+    if (p.counts || p.rows) {
         s.bn = p.bn;
         s.cap = p.cap;
         // CTAs per item: each at least four column blocks; eight for a few rows, which leave SMs idle
@@ -878,15 +983,20 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
         const int most = s.n <= 16 ? 8 : 4;
         while (s.split < most && p.kblocks >= 8 * s.split) s.split *= 2;
         // clusters per tile: as many as it can have items, or as fill the SMs about four times over
-        const int items = p.cap + p.bn / kShRows, fill = 4 * n_sm / (s.split * p.row_tiles);
+        const int items = p.cap + p.bn / (p.rows ? 16 : 64), fill = 4 * n_sm / (s.split * p.row_tiles);
         const int y = items < fill ? items : fill < 4 ? 4 : fill;
         const dim3 grid(s.split, y, p.row_tiles);
         const int nt = (p.rank + 7) / 8;
-        e = nt <= 2 ? shrink_launch<2>(s, grid, st) : nt <= 4 ? shrink_launch<4>(s, grid, st)
-            : nt <= 8 ? shrink_launch<8>(s, grid, st) : shrink_launch<16>(s, grid, st);
+        if (p.rows)
+            e = nt <= 2 ? shrink_launch<2, 16>(s, grid, st) : nt <= 4 ? shrink_launch<4, 16>(s, grid, st)
+                : nt <= 8 ? shrink_launch<8, 16>(s, grid, st) : shrink_launch<16, 16>(s, grid, st);
+        else
+            e = nt <= 2 ? shrink_launch<2, 64>(s, grid, st) : nt <= 4 ? shrink_launch<4, 64>(s, grid, st)
+                : nt <= 8 ? shrink_launch<8, 64>(s, grid, st) : shrink_launch<16, 64>(s, grid, st);
         if (e != cudaSuccess) return e;
     }
-    const auto kernel = wk.pair ? k_project_pair : k_project;
+    const auto kernel = p.rows ? (wk.pair ? k_project_pair<true> : k_project<true>)
+                               : (wk.pair ? k_project_pair<false> : k_project<false>);
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem + 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -904,7 +1014,7 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
         at[na].val.clusterDim.y = at[na].val.clusterDim.z = 1;
         ++na;
     }
-    if (p.counts) {
+    if (p.counts || p.rows) {
         at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[na].val.programmaticStreamSerializationAllowed = 1;
         ++na;
