@@ -277,11 +277,12 @@ static void norm_launch_v(const AddNormArgs& a, bool vec, int ch, dim3 grid, dim
 
 cudaError_t launch_add_rmsnorm(AddNormArgs a, bool x_bf16, int res_kind, bool vec, int n_sm, cudaStream_t st) {
     const int blocks = (a.H + kBlk - 1) / kBlk;
-    // Few rows: one block per warp, the shortest chain.  Many: four blocks per
-    // warp, fewer threads per row and more rows in flight.
-    // (A hidden size of at most 16,384 is 64 blocks: 16 warps of four.)
-    int ch = a.n < 2 * n_sm && blocks <= 32 ? 1 : 4;
-    if (blocks < ch) ch = blocks >= 2 ? 2 : 1;
+    // Few rows: one block per warp, the shortest chain.  Many: two, so that a
+    // row's loads are in flight at once (4096 columns, 11,709 rows with every
+    // output: 123 us; one block 156 us, four 145 us).  More than 32 blocks (8192
+    // columns) need four to fit a CTA.
+    int ch = blocks > 32 ? 4 : a.n < 2 * n_sm ? 1 : 2;
+    if (blocks < ch) ch = 1;
     a.warps_per_row = (blocks + ch - 1) / ch;
     const bool solo = a.warps_per_row == 1;
     const int rows_per_cta = solo ? 4 : 1;
@@ -318,76 +319,116 @@ __device__ __forceinline__ void widen4(uint32_t w, int fmt, float (&v)[4]) {
 }
 }  // namespace
 
-template <bool OBF>
-__global__ void __launch_bounds__(256) k_widen_rows(const uint8_t* q, int fmt, const float* scale, int group, int H,
-                                                    int64_t total, void* out) {
-    const int64_t i0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16;
-    if (i0 >= total) return;
-    const int ngroups = group ? (H + group - 1) / group : 1;
-    int64_t row = i0 / H;
-    int c = (int)(i0 - row * H);
-    const int cnt = total - i0 < 16 ? (int)(total - i0) : 16;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (cnt == 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q + i0));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
+// I: the type of flat indices (32 bits where they suffice: the division by the
+// row width costs as much as the rest otherwise).  A thread's pieces are in
+// flight together: two where there are enough threads all the same (11,709 x
+// 4096 to bf16: 24.0 us, one 32.5 us), one for few rows (61 x 2050 to binary32:
+// 2.9 us, two 3.8 us).
+template <bool OBF, typename I, int kWidenPieces>
+__global__ void __launch_bounds__(256) k_widen_rows(const uint8_t* q, int fmt, const float* scale, int shift, int H,
+                                                    I total, void* out) {
+    const int ngroups = shift ? (H + (1 << shift) - 1) >> shift : 1;
+    uint4 raw[kWidenPieces];
+    float first[kWidenPieces];
+    I row[kWidenPieces];
+    int col[kWidenPieces];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < cnt) w[j >> 2] |= (uint32_t)q[i0 + j] << (8 * (j & 3));
+    for (int p = 0; p < kWidenPieces; ++p) {
+        const I i0 = ((I)blockIdx.x * (256 * kWidenPieces) + p * 256 + threadIdx.x) * 16;
+        raw[p] = make_uint4(0, 0, 0, 0);
+        row[p] = 0, col[p] = 0, first[p] = 0.f;
+        if (i0 < total) {
+            if (total - i0 >= 16) {
+                raw[p] = ld_stream_v4(q + i0);
+            } else {
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j < (int)(total - i0)) w[j >> 2] |= (uint32_t)q[i0 + j] << (8 * (j & 3));
+                raw[p] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            row[p] = i0 / (I)H;
+            col[p] = (int)(i0 - row[p] * (I)H);
+            first[p] = __ldg(scale + (size_t)row[p] * ngroups + (shift ? col[p] >> shift : 0));
+        }
     }
-    float v[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float t[4];
-        widen4(w[j], fmt, t);
+    for (int p = 0; p < kWidenPieces; ++p) {
+        const I i0 = ((I)blockIdx.x * (256 * kWidenPieces) + p * 256 + threadIdx.x) * 16;
+        if (i0 >= total) return;
+        const int cnt = total - i0 < 16 ? (int)(total - i0) : 16;
+        const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
+        float v[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * j + e] = t[e];
-    }
-    float sc = __ldg(scale + row * ngroups + (group ? c / group : 0));
-    // columns up to the end of this scale's group
-    int left = (group ? min(H, (c / group + 1) * group) : H) - c;
-    if (left >= cnt) {
+        for (int j = 0; j < 4; ++j) {
+            float t[4];
+            widen4(w[j], fmt, t);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], sc);
-    } else {
-        int gi = group ? c / group : 0;
+            for (int e = 0; e < 4; ++e) v[4 * j + e] = t[e];
+        }
+        float sc = first[p];
+        // columns up to the end of this scale's group
+        int g = shift ? col[p] >> shift : 0;
+        int left = (shift ? min(H, (g + 1) << shift) : H) - col[p];
+        if (left >= cnt) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (j < cnt) {
-                if (left == 0) {
-                    if (++gi == ngroups) gi = 0, ++row;
-                    sc = __ldg(scale + row * ngroups + gi);
-                    left = group ? min(group, H - gi * group) : H;
+            for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], sc);
+        } else {
+            size_t r = row[p];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (j < cnt) {
+                    if (left == 0) {
+                        if (++g == ngroups) g = 0, ++r;
+                        sc = __ldg(scale + r * ngroups + g);
+                        left = shift ? min(1 << shift, H - (g << shift)) : H;
+                    }
+                    v[j] = __fmul_rn(v[j], sc);
+                    --left;
                 }
-                v[j] = __fmul_rn(v[j], sc);
-                --left;
             }
         }
-    }
-    if (cnt == 16) {
-        if constexpr (OBF) {
-            st_global_v8(static_cast<uint16_t*>(out) + i0, bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                         bf16x2(v[6], v[7]), bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]),
-                         bf16x2(v[14], v[15]));
+        if (cnt == 16) {
+            if constexpr (OBF) {
+                st_global_v8(static_cast<uint16_t*>(out) + i0, bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                             bf16x2(v[6], v[7]), bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]),
+                             bf16x2(v[14], v[15]));
+            } else {
+                float* o = static_cast<float*>(out) + i0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<float4*>(o)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
         } else {
-            float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + i0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            for (int j = 0; j < 16; ++j)
+                if (j < cnt) store1(out, OBF, i0 + j, v[j]);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < cnt) store1(out, OBF, i0 + j, v[j]);
     }
+}
+
+template <bool OBF, int P>
+static void widen_launch(const uint8_t* q, int fmt, const float* scale, int shift, int H, int64_t total, void* out,
+                         cudaStream_t st) {
+    const int64_t per = 256 * P * 16, ctas = (total + per - 1) / per;
+    if (ctas * per < ((int64_t)1 << 32))
+        k_widen_rows<OBF, uint32_t, P><<<(unsigned)ctas, 256, 0, st>>>(q, fmt, scale, shift, H, (uint32_t)total, out);
+    else
+        k_widen_rows<OBF, uint64_t, P><<<(unsigned)ctas, 256, 0, st>>>(q, fmt, scale, shift, H, (uint64_t)total, out);
 }
 
 cudaError_t launch_widen_rows(const uint8_t* q, int fmt, const float* scale, int group, int n, int H, void* out,
                               bool out_bf16, cudaStream_t st) {
+    const int shift = group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : 0;
     const int64_t total = (int64_t)n * H;
-    const int64_t ctas = (total + 16 * 256 - 1) / (16 * 256);
-    if (out_bf16) k_widen_rows<true><<<(unsigned)ctas, 256, 0, st>>>(q, fmt, scale, group, H, total, out);
-    else k_widen_rows<false><<<(unsigned)ctas, 256, 0, st>>>(q, fmt, scale, group, H, total, out);
+    const bool few = total < ((int64_t)1 << 22);   // 1,024 CTAs of one piece per thread
+    if (out_bf16) {
+        if (few) widen_launch<true, 1>(q, fmt, scale, shift, H, total, out, st);
+        else widen_launch<true, 2>(q, fmt, scale, shift, H, total, out, st);
+    } else {
+        if (few) widen_launch<false, 1>(q, fmt, scale, shift, H, total, out, st);
+        else widen_launch<false, 2>(q, fmt, scale, shift, H, total, out, st);
+    }
     return cudaGetLastError();
 }
 
