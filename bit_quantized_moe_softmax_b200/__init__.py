@@ -314,17 +314,25 @@ def _refuse(where: str, msg: str):
 
 def _tensors(where: str, dev: int, specs):
     """Each (name, tensor or None, shape, types): on CUDA device dev, contiguous, of that shape and one of the types."""
-    for name, t, shape, types in specs:
-        if t is None or (t.dtype in types and t.shape == shape and t.get_device() == dev and t.is_contiguous()
-                         and dev >= 0):
-            continue
+    for _, t, shape, types in specs:
+        if t is not None and not (t.dtype in types and t.shape == shape and t.get_device() == dev
+                                  and t.is_contiguous()) or dev < 0:
+            break
+    else:
+        return
+    given = [s for s in specs if s[1] is not None]
+    for name, t, _, types in given:
         if t.dtype not in types:
             _refuse(where, "%s: unsupported type %s" % (name, t.dtype))
+    for name, t, shape, _ in given:
         if t.shape != shape:
             _refuse(where, "%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+    for name, t, _, _ in given:
         if dev < 0 or t.get_device() != dev:
             _refuse(where, "%s: on %s, expected one CUDA device for all" % (name, t.device))
-        _refuse(where, "%s: not contiguous" % name)
+    for name, t, _, _ in given:
+        if not t.is_contiguous():
+            _refuse(where, "%s: not contiguous" % name)
 
 
 def _call(where: str, dev: int, stream, fn, *args):

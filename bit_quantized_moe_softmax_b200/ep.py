@@ -9,6 +9,8 @@ a rank holds:
   the slot's expert id, to the rank that owns that expert; rows leave in
   (destination rank, slot index) order, so every rank receives its rows
   grouped by source rank and, within a source, in slot order;
+  (``dispatch_q8`` sends the rows as 8-bit codes with their scales, as
+  ds4moe_add_rmsnorm leaves them: about a quarter of binary32's bytes);
 * the owning ranks run their experts on the rows they received (a function
   the caller passes in: one output row per input row);
 * combine -- the results travel back along the reverse route and the home
@@ -98,6 +100,18 @@ def dispatch(x: torch.Tensor, ids: torch.Tensor, p: DispatchPlan, group=None):
             _exchange(eid, R, p.send_counts, p.recv_counts, group))
 
 
+def dispatch_q8(q: torch.Tensor, scale: torch.Tensor, ids: torch.Tensor, p: DispatchPlan, group=None):
+    """``dispatch`` of 8-bit rows: codes q [n, H] (float8_e4m3fn or int8) and scales [n, groups].
+
+    Returns (codes [R, H], scales [R, groups], row_expert [R] int64)."""
+    at = p.order // p.k
+    eid = ids.reshape(-1)[p.order].to(torch.int64)
+    R = int(sum(p.recv_counts))
+    codes = _exchange(q.view(torch.uint8)[at], R, p.send_counts, p.recv_counts, group)
+    return (codes.view(q.dtype), _exchange(scale[at], R, p.send_counts, p.recv_counts, group),
+            _exchange(eid, R, p.send_counts, p.recv_counts, group))
+
+
 def combine(y_rows: torch.Tensor, w: torch.Tensor, p: DispatchPlan, base: torch.Tensor, group=None):
     """out[t] = base[t] + sum_j w[t, j] * y[t*k + j], j ascending.
 
@@ -122,6 +136,17 @@ def moe_forward_ep(x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, E: int, 
     rows, eid = dispatch(x, ids, p, group)
     y = local_fn(rows, eid) if rows.shape[0] else rows.new_zeros((0,) + tuple(base.shape[1:]))
     return combine(y, w, p, base, group)
+
+
+def moe_forward_ep_q8(q: torch.Tensor, scale: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, E: int, local_fn,
+                      base: torch.Tensor, group=None, combine_fn=combine) -> torch.Tensor:
+    """``moe_forward_ep`` with 8-bit rows on the way to the experts: local_fn(codes, scales, row_expert) -> [R, H].
+
+    combine_fn: ``combine`` or ``combine_gpu``."""
+    p = plan(ids, E, group)
+    codes, scales, eid = dispatch_q8(q, scale, ids, p, group)
+    y = local_fn(codes, scales, eid) if codes.shape[0] else scales.new_zeros((0,) + tuple(base.shape[1:]))
+    return combine_fn(y, w, p, base, group)
 
 
 # ------------------------------------------------------------------ GPU halves (one rank's device work)
@@ -164,6 +189,16 @@ class GpuExpertShard:
             b = min(R, a + self.max_rows)
             ds4moe_forward_routed(self.lay.h, rows[a:b].contiguous(), ids[a:b], ones[a:b], out[a:b])
         return out
+
+    def forward_q8(self, codes: torch.Tensor, scales: torch.Tensor, row_expert: torch.Tensor,
+                   columns: int = 128) -> torch.Tensor:
+        """The experts on 8-bit rows (codes [R, H], one scale per ``columns`` columns; 0: per row), widened to
+        binary32 by ds4moe_widen_rows."""
+        from . import ds4moe_widen_rows
+
+        rows = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
+        ds4moe_widen_rows(codes, scales, rows, group=columns)
+        return self(rows, row_expert)
 
 
 def combine_gpu(y_rows: torch.Tensor, w: torch.Tensor, p: DispatchPlan, base: torch.Tensor, group=None):
