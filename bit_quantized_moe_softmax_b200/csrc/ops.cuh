@@ -49,7 +49,7 @@ struct SampleArgs {
     float* probs;         // [n][V] or nullptr
     int slice, seg;       // tokens per CTA and per warp, set by the launcher
 };
-cudaError_t launch_sample(SampleArgs a, bool bf16, int n, cudaStream_t st);
+cudaError_t launch_sample(SampleArgs a, bool bf16, int n, int n_sm, cudaStream_t st);
 
 struct ShrinkArgs {
     const __nv_bfloat16* x;     // [n][fin]

@@ -230,7 +230,10 @@ ds4moe_status ds4moe_sample(const void* d_logits, int32_t dtype, int64_t row_str
     SampleArgs a{};
     a.logits = d_logits, a.ld = row_stride, a.V = vocab, a.temp = d_temperature, a.top_k = d_top_k, a.top_p = d_top_p;
     a.min_p = d_min_p, a.u = d_u, a.token = d_token, a.prob = d_prob, a.probs = d_probs;
-    return done(launch_sample(a, dtype == DS4MOE_ACT_BF16, n, (cudaStream_t)stream), "sample launch");
+    int n_sm = 0;
+    const cudaError_t ce = sm_count(&n_sm);
+    if (ce != cudaSuccess) return done(ce, "sample: device");
+    return done(launch_sample(a, dtype == DS4MOE_ACT_BF16, n, n_sm, (cudaStream_t)stream), "sample launch");
 }
 
 }  // extern "C"

@@ -33,7 +33,7 @@ namespace {
 constexpr int kST = 512;             // threads
 constexpr int kSW = kST / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr int kList = kST;                  // tokens of one bin that are put in order at once
 constexpr int kTab = 128;                   // entries of the table of 2^(j / 128)
@@ -46,7 +46,6 @@ typedef unsigned long long u64;
 struct __align__(16) SampleSmem {
     uint32_t hist[2][2][kBins];      // two in turn: counts in the first array, or the low and high words of weights
     u64 group[2][kMaxCluster][32];   // sums of 64 bins of each CTA, written by the peers; two in turn
-    u64 part[kMaxCluster][64];       // one group's bins of each CTA
     u64 list[kList];                 // this CTA's tokens of a bin (the first kList / C), then all of them in order
     uint32_t listed[kMaxCluster];    // how many there are in each CTA
     uint32_t list_n;
@@ -163,16 +162,17 @@ __device__ __noinline__ void find_bin(SampleSmem& S, int buf, bool wide, u64 tar
     group_scan<C>(S, buf, lane, inc, mine);
     const int g = __ffs(__ballot_sync(kAll, inc >= target)) - 1;
     before = __shfl_sync(kAll, inc - mine, g);
+    u64(*part)[64] = reinterpret_cast<u64(*)[64]>(S.hist[buf ^ 1]);   // whose readers have passed a barrier
     for (int i = tid; i < 64 * C; i += kST) {
         const uint32_t* h = cl.map_shared_rank(&S.hist[0][0][0], i >> 6) + 2 * buf * kBins + g * 64 + (i & 63);
         const uint32_t lo = h[0], hi = wide ? h[kBins] : 0u;
-        S.part[i >> 6][i & 63] = (u64)lo | ((u64)hi << 32);
+        part[i >> 6][i & 63] = (u64)lo | ((u64)hi << 32);
     }
     __syncthreads();
     u64 a = 0, b = 0;   // bins 2 lane, 2 lane + 1
 #pragma unroll
     for (int p = 0; p < C; ++p) {
-        const ulonglong2 v = reinterpret_cast<const ulonglong2*>(S.part[p])[lane];
+        const ulonglong2 v = reinterpret_cast<const ulonglong2*>(part[p])[lane];
         a += v.x, b += v.y;
     }
     inc = warp_scan(a + b, lane);
@@ -183,7 +183,7 @@ __device__ __noinline__ void find_bin(SampleSmem& S, int buf, bool wide, u64 tar
     bin = __shfl_sync(kAll, (uint32_t)(g * 64 + 2 * lane + second), at);
     own = __shfl_sync(kAll, second ? b : a, at);
     before = __shfl_sync(kAll, pre, at);
-    __syncthreads();   // S.part is free again
+    __syncthreads();   // part is free again
 }
 
 // A token in the order of the filters, largest first: key, then the lower index.
@@ -338,40 +338,40 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
             if (mass) h[kST + tid] = make_uint4(0, 0, 0, 0);
             if (tid == 0) S.list_n = 0;
             __syncthreads();
-            auto bin_of = [&](float l) -> uint32_t {   // kBins or more: not in this round
-                if (round == 0) return coarse(l);
-                const uint32_t k = order_key(l);
-                return k - lo <= hi - lo ? (hi - k) >> shift : kAll;
+            auto put = [&](uint32_t b, u64 v) {
+                const uint32_t x = (uint32_t)v, old = atomicAdd(&S.hist[buf][0][b], x);
+                const uint32_t y = (uint32_t)(v >> 32) + (old + x < x);   // with the carry
+                if (y) atomicAdd(&S.hist[buf][1][b], y);
             };
-            if (mass) {
-                each([&](const float (&l)[4], int i) {
-                    uint32_t b[4];
-                    bool any = false;
+            if (round == 0) {
+                each([&](const float (&l)[4], int) {
+                    // (after top-k most steps hold nothing)
+                    if (!__any_sync(kAll, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) > kNegInf)) return;
+                    if (mass) {
+                        u64 v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        b[e] = inside(l[e], i + e) ? bin_of(l[e]) : kAll;
-                        any |= b[e] < kBins;
-                    }
-                    if (!__any_sync(kAll, any)) return;
-                    u64 v[4];
+                        for (int e = 0; e < 4; ++e) v[e] = weigh.units(l[e]);   // none at -infinity
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = weigh.units(l[e]);
+                        for (int e = 0; e < 4; ++e)
+                            if (v[e]) put(coarse(l[e]), v[e]);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (b[e] < kBins && v[e]) {
-                            const uint32_t x = (uint32_t)v[e];
-                            const uint32_t old = atomicAdd(&S.hist[buf][0][b[e]], x);
-                            const uint32_t y = (uint32_t)(v[e] >> 32) + (old + x < x);   // with the carry
-                            if (y) atomicAdd(&S.hist[buf][1][b[e]], y);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            if (l[e] > kNegInf) atomicAdd(&S.hist[buf][0][coarse(l[e])], 1u);
                     }
                 });
             } else {
-                each([&](const float (&l)[4], int i) {
+                each([&](const float (&l)[4], int) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint32_t b = l[e] != kNegInf ? bin_of(l[e]) : kAll;
-                        if (b < kBins) atomicAdd(&S.hist[buf][0][b], 1u);
+                        const uint32_t k = order_key(l[e]);
+                        if (k - lo > hi - lo) continue;
+                        if (!mass) {
+                            atomicAdd(&S.hist[buf][0][(hi - k) >> shift], 1u);
+                        } else {
+                            const u64 v = weigh.units(l[e]);
+                            if (v) put((hi - k) >> shift, v);
+                        }
                     }
                 });
             }
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                     bool in[4], any = false;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        in[e] = coarse(l[e]) == bin && inside(l[e], i + e);
+                        in[e] = coarse(l[e]) == bin && l[e] > kNegInf;
                         any |= in[e];
                     }
                     if (!__any_sync(kAll, any)) return;
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
             const float at = key_value(hi);
             const u64 w = mass ? weigh.units(at) : 1;
             const u64 q = (target - before + w - 1) / w;
-            if (q >= own / w) {   // all of those that were left; at an earlier threshold its last index stays
-                last = at == thr ? last : 0x7fffffff;
+            if (q >= own / w) {   // all of those that were left
+                last = 0x7fffffff;
             } else {
                 uint32_t t = 0;
                 each([&](const float (&l)[4], int i) {
@@ -508,6 +508,19 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                 last = S.tie_at;
             }
             thr = at;
+        }
+        if (!mass && by_p) {   // what top-k removes is gone for top-p
+            each([&](const float (&l)[4], int i) {
+                if (!__any_sync(kAll, l[0] > kNegInf || l[1] > kNegInf || l[2] > kNegInf || l[3] > kNegInf)) return;
+                float4 v;
+                v.x = inside(l[0], i) ? l[0] : kNegInf;
+                v.y = inside(l[1], i + 1) ? l[1] : kNegInf;
+                v.z = inside(l[2], i + 2) ? l[2] : kNegInf;
+                v.w = inside(l[3], i + 3) ? l[3] : kNegInf;
+                *reinterpret_cast<float4*>(vals + i) = v;
+            });
+            // (each thread reads its own tokens in the passes that follow, the search for a tie a warp's)
+            __syncwarp();
         }
     }
 
@@ -645,8 +658,8 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
 
 template <bool BF, int C>
 static cudaError_t sample_launch(const SampleArgs& a, int n, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(k_sample<BF, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSampleMaxVocab / kMaxCluster * 4);
+    cudaError_t e = cudaFuncSetAttribute(k_sample<BF, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSampleMaxVocab / 8 * 4);
+    if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(k_sample<BF, C>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)n * C);
@@ -662,22 +675,23 @@ static cudaError_t sample_launch(const SampleArgs& a, int n, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, k_sample<BF, C>, a);
 }
 
-cudaError_t launch_sample(SampleArgs a, bool bf16, int n, cudaStream_t st) {
-    // CTAs per row: a quarter to the whole of a CTA's 32,768-token share each
+template <bool BF>
+static cudaError_t sample_any(const SampleArgs& a, int C, int n, cudaStream_t st) {
+    if (C == 1) return sample_launch<BF, 1>(a, n, st);
+    if (C == 2) return sample_launch<BF, 2>(a, n, st);
+    if (C == 4) return sample_launch<BF, 4>(a, n, st);
+    if (C == 8) return sample_launch<BF, 8>(a, n, st);
+    return sample_launch<BF, 16>(a, n, st);
+}
+
+cudaError_t launch_sample(SampleArgs a, bool bf16, int n, int n_sm, cudaStream_t st) {
+    // CTAs per row: a quarter to the whole of a CTA's 32,768-token share each; for a few rows twice as many
     int C = 1;
-    while (C < kMaxCluster && (a.V + C - 1) / C > 8192) C *= 2;
+    while (C < 8 && (a.V + C - 1) / C > 8192) C *= 2;
+    if (C == 8 && a.V > 65536 && n * 16 <= n_sm / 2) C = 16;
     a.slice = (((a.V + C - 1) / C) + 7) & ~7;
     a.seg = ((a.slice + kSW - 1) / kSW + 127) & ~127;
-    if (bf16) {
-        if (C == 1) return sample_launch<true, 1>(a, n, st);
-        if (C == 2) return sample_launch<true, 2>(a, n, st);
-        if (C == 4) return sample_launch<true, 4>(a, n, st);
-        return sample_launch<true, 8>(a, n, st);
-    }
-    if (C == 1) return sample_launch<false, 1>(a, n, st);
-    if (C == 2) return sample_launch<false, 2>(a, n, st);
-    if (C == 4) return sample_launch<false, 4>(a, n, st);
-    return sample_launch<false, 8>(a, n, st);
+    return bf16 ? sample_any<true>(a, C, n, st) : sample_any<false>(a, C, n, st);
 }
 
 }  // namespace ds4
