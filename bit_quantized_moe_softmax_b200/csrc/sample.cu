@@ -42,6 +42,7 @@ constexpr double kMagic = 6755399441055744.0;   // 1.5 * 2^52: adding it leaves 
 constexpr float kNegInf = -INFINITY;
 
 typedef unsigned long long u64;
+constexpr u64 kOffset = 0x4338000000000000ull;   // kMagic's bits
 
 struct __align__(16) SampleSmem {
     uint32_t hist[2][2][kBins];      // two in turn: counts in the first array, or the low and high words of weights
@@ -70,33 +71,50 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(
 // exp((l - M) / T) of one token in binary64: 2^(y / 128), y = (l - M) 128
 // log2(e) / T, from a table of 2^(j / 128) and four terms of the series of
 // 2^(r / 128), |r| <= 1/2 (a little more, as binary32 finds the nearest
-// integer): the fifth is below 2e-15, a twentieth of the unit 2^-44.  Ten
-// binary64 operations; 16,384 tokens take 3,500 clocks of an SM (CUDA's own
-// exp: twice that).  Free of branches, so that several are in flight.  The
-// result is not used for l = -infinity.
+// integer): the fifth is below 2e-15, a twentieth of the unit 2^-44.  What
+// bounds the passes over the weights is the issue of their instructions, so
+// every one counts: the integer n comes from a binary32 addition and is used
+// with its offset (which the table index and the exponent drop by themselves),
+// logits far below are raised to where the weight is 2^-64 instead of being
+// tested for, and the unit's sums keep the offset of the conversion.
 struct Weigh {
-    double M, c;           // c = 128 log2(e) / T
+    double M, c;           // c = 128 log2(e) / T, at most where one step below M already weighs nothing
     float Mf, cf;
+    float low;             // M - 8192 / c
+    bool flat;             // T so large that low is the lowest binary32 value: -infinity is tested for
     const double* tab;
+
+    __device__ void set(float m, float T, const double* table) {
+        const float below = __uint_as_float(m > 0.f ? __float_as_uint(m) - 1 : m < 0.f ? __float_as_uint(m) + 1 : 0x80000001u);
+        M = m, Mf = m, tab = table;
+        c = fmin(fmin(kTab * 1.44269504088896340736 / (double)T, 6000.0 / ((double)m - (double)below)), 1e38);
+        cf = (float)c;
+        const double l = (double)m - 8192.0 / c;   // (c = 0: -infinity)
+        flat = !(l > -3.4e38);
+        low = flat ? -3.402823466e38f : __double2float_rd(l);
+    }
     __device__ __forceinline__ double operator()(float l) const {
-        // the nearest integer by a binary32 addition (an F2I has an eighth of its rate); -8192 and NaN weigh nothing
-        const int k = __float_as_int(fmaxf((l - Mf) * cf, -8192.f) + 12582912.f) - 0x4b400000;
-        const double kd = __hiloint2double(0x43380000 + (k >> 31), k) - kMagic;
-        const double r = fma((double)l - M, c, -kd);
+        l = fmaxf(l, low);
+        const int n = __float_as_int(fmaf(l - Mf, cf, 12582912.f));        // 0x4b400000 + the nearest integer of y
+        const double k = __hiloint2double(0x43300000, n) - (4503599627370496.0 + 1262485504.0);
+        const double r = fma((double)l - M, c, -k);
         constexpr double h = 0.69314718055994530942 / kTab;
         double p = fma(r, h * h * h * h / 24.0, h * h * h / 6.0);
         p = fma(r, p, h * h / 2.0);
         p = fma(r, p, h);
         p *= r;
-        double w = tab[k & (kTab - 1)];
+        double w = tab[n & (kTab - 1)];
         w = fma(w, p, w);
-        w = __hiloint2double(__double2hiint(w) + ((k >> 7) << 20), __double2loint(w));
-        return k < -46 * kTab ? 0.0 : w;   // below half a unit by far
+        return __hiloint2double(__double2hiint(w) + ((n & ~(kTab - 1)) << 13), __double2loint(w));
     }
-    static __device__ __forceinline__ u64 to_units(double w) {
-        return (u64)(__double_as_longlong(fma(w, kOne, kMagic)) - __double_as_longlong(kMagic));
+    static __device__ __forceinline__ u64 offset_units(double w) { return (u64)__double_as_longlong(fma(w, kOne, kMagic)); }
+    static __device__ __forceinline__ u64 to_units(double w) { return offset_units(w) - kOffset; }
+    // of any token
+    __device__ __forceinline__ u64 units(float l) const {
+        u64 v = to_units((*this)(l));
+        if (flat && l == kNegInf) v = 0;
+        return v;
     }
-    __device__ __forceinline__ u64 units(float l) const { return to_units((*this)(l)); }
 };
 
 // Bin of the first histogram: (M - l) in steps, the last bin for all beyond.
@@ -302,8 +320,9 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
     }
     const bool by_k = K >= 1 && K < a.V, by_p = P < 1.f, by_m = mp > 0.f;
     const double minw = fmin((double)mp, 1.0);
-    const double inv = 1.0 / (double)T, c = inv * (kTab * 1.44269504088896340736);
-    const Weigh weigh{(double)mx, c, mx, (float)fmin(c, 1e38), S.tab};
+    const double inv = 1.0 / (double)T;
+    Weigh weigh;
+    weigh.set(mx, T, S.tab);
     const int s0 = warp * a.seg;   // this warp's tokens: s0 .. s0 + seg - 1
 
     // ---- the prefix that top-k and top-p keep: tokens above thr, and those at it up to index last of the row
@@ -351,9 +370,16 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                         u64 v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[e] = weigh.units(l[e]);   // none at -infinity
+                        uint32_t b[4], old[4];   // the four additions in flight together, then their carries
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (v[e]) put(coarse(l[e]), v[e]);
+                        for (int e = 0; e < 4; ++e) b[e] = coarse(l[e]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) old[e] = v[e] ? atomicAdd(&S.hist[buf][0][b[e]], (uint32_t)v[e]) : 0u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t y = (uint32_t)(v[e] >> 32) + (old[e] + (uint32_t)v[e] < (uint32_t)v[e]);
+                            if (y) atomicAdd(&S.hist[buf][1][b[e]], y);
+                        }
                     } else {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
@@ -582,14 +608,21 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
             __syncwarp();
         });
         flush(lane < n);
-    } else {
-#pragma unroll 2
+    } else if (by_m || weigh.flat) {
         for (int i = s0 + 4 * lane; i < s0 + a.seg; i += 128) {
             double w[4];
             kept(i, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum += Weigh::to_units(w[e]);
         }
+    } else {
+#pragma unroll 2
+        for (int i = s0 + 4 * lane; i < s0 + a.seg; i += 128) {
+            const float4 v = *reinterpret_cast<const float4*>(vals + i);
+            sum += Weigh::offset_units(weigh(v.x)) + Weigh::offset_units(weigh(v.y));
+            sum += Weigh::offset_units(weigh(v.z)) + Weigh::offset_units(weigh(v.w));
+        }
+        sum -= (u64)(a.seg / 32) * kOffset;   // seg / 32 tokens a lane
     }
     sum = warp_sum(sum);
     __syncthreads();   // S.wsum of find_bin has been read
