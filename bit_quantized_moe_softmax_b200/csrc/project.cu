@@ -33,7 +33,7 @@ constexpr int kPMaxStages = 10;
 constexpr int kAhead = 16;
 constexpr int kRowsMin = 8, kRowsMax = 64;   // rows whose adapters the draining warps add
 constexpr int kPSmem = 200 * 1024;       // of 227 KB
-constexpr int kPSmemRows = 168 * 1024;   // beside a CTA of the first kernel
+constexpr int kPSmemRows = 168 * 1024, kPSmemEntries = 150 * 1024;   // beside a CTA of the first kernel
 
 // Error word of the projection's bounded waits, one per device.
 __device__ uint32_t g_project_err;
@@ -93,8 +93,9 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool i
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+// (NT 8 bounded as if for more threads: 96 registers, so that two fit beside a CTA of the projection)
 template <int NT, int kShRows>   // 8-wide rank blocks; rows per item
-__global__ void __launch_bounds__(256, NT >= 8 ? 2 : NT == 4 ? 4 : 5) k_adapter_shrink(ShrinkArgs a) {
+__global__ void __launch_bounds__(NT == 8 ? 320 : 256, NT >= 8 ? 2 : NT == 4 ? 4 : 5) k_adapter_shrink(ShrinkArgs a) {
     extern __shared__ __align__(128) unsigned char ring[];   // [kShStages][kShRows + 8 NT rows][128 bytes]
     __shared__ __align__(16) int s_id[256];
     __shared__ int s_w[8], s_rank[256], s_adapter[256], s_n[256], s_rows[kShRows], s_j, s_c0, s_cnt;
@@ -385,6 +386,45 @@ __device__ __forceinline__ void store16(const ProjectArgs& a, const uint32_t (&v
     }
 }
 
+// Rows c0 .. c1 - 1 of a split tile's 128 features from o on, finished by the
+// calling warp and its `warps` - 1 peers: the partial sums [bn][128] in the
+// shared memory (at `sums`) of ranks rank0, rank0 + step, .. of the cluster, in
+// that order.  A lane has four features, so that a warp's loads and stores are
+// wide and few enough to wait for.
+__device__ __forceinline__ void finish_split(const ProjectArgs& a, cg::cluster_group& cl, float* sums, int rank0, int step, int o,
+                                             int r0, int c0, int c1, int warp, int warps, int lane) {
+    const float* part[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) part[p] = cl.map_shared_rank(sums, rank0 + (p < a.split ? p : 0) * step);
+    const bool wide = (a.fout & 3) == 0;   // else features lane, lane + 32, ..: stores next to each other
+#pragma unroll 2
+    for (int c = c0 + warp; c < c1; c += warps) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            if (p < a.split) {
+                const float* q = part[p] + c * kPM;
+                if (wide) {
+                    const float4 x = reinterpret_cast<const float4*>(q)[lane];
+                    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += q[32 * e + lane];
+                }
+            }
+        }
+        __nv_bfloat16* d = a.out + (size_t)(r0 + c) * a.fout + o;
+        if (wide) {
+            if (o + 4 * lane < a.fout)
+                *reinterpret_cast<uint2*>(d + 4 * lane) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (o + 32 * e + lane < a.fout) d[32 * e + lane] = __float2bfloat16_rn(v[e]);
+        }
+    }
+}
+
 // A tile's accumulators (columns from taddr on) to out, with what the adapters
 // add to up to 64 rows (acc).  Not ok (a wait ran out): NaN.
 template <bool Rows, int N>
@@ -624,20 +664,9 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
         __syncwarp();
         cg::cluster_group cl = cg::this_cluster();
         cl.sync();
-        const int tile = first;
-        const int o = tile / a.row_tiles * kPM + (tid & 127), r0 = tile % a.row_tiles * a.bn;
-        const int per = (a.bn + a.split - 1) / a.split;
-        const int c1 = min(min(a.bn, a.n - r0), per * (rank_in + 1));
-        const float* part[8];
-#pragma unroll
-        for (int p = 0; p < 8; ++p) part[p] = cl.map_shared_rank(reinterpret_cast<const float*>(st), p < a.split ? p : 0) + (tid & 127);
-        for (int c = per * rank_in + (tid >> 7); c < c1; c += 2) {
-            float v = 0.f;
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-                if (p < a.split) v += part[p][c * kPM];
-            if (o < a.fout) a.out[(size_t)(r0 + c) * a.fout + o] = __float2bfloat16_rn(v);
-        }
+        const int r0 = first % a.row_tiles * a.bn, per = (a.bn + a.split - 1) / a.split;
+        finish_split(a, cl, reinterpret_cast<float*>(st), 0, 1, first / a.row_tiles * kPM, r0, per * rank_in,
+                     min(min(a.bn, a.n - r0), per * (rank_in + 1)), warp, kPThreads / 32, lane);
         cl.sync();   // peers have read this CTA's sums
     }
     if (Rows || a.counts) griddep_wait();   // this grid's end implies the first one's
@@ -658,6 +687,7 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
 // 128 r .. of each 256 features and half of x's rows; the leader's thread
 // issues for both.  Both accumulators (2 x bn columns) are in use, so a tile's
 // epilogue is not overlapped; eight warps drain it, four per accumulator.
+// Split tiles as above: up to four pairs in a cluster, each a part of the K axis.
 struct PairSmem {
     uint64_t full[kPMaxStages], empty[kPMaxStages];
     uint64_t accF, accE[2];
@@ -668,9 +698,9 @@ struct PairSmem {
 };
 constexpr int kPairThreads = 384;   // warps: 0 TMA, 1 MMA (leader), 2 TMEM, 4..11 epilogue
 
-__device__ __forceinline__ uint32_t map_rank0(uint32_t addr) {
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, int rank) {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
 // Tiled loads of a pair: into this CTA's shared memory, completing on the leader's barrier.
@@ -695,30 +725,33 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t da, uint64_t db, u
         : "memory");
 }
 // Arrive on the barrier at this offset in both CTAs when the MMAs issued so far have completed.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
-    const uint16_t both = 3;
+__device__ __forceinline__ void pair_commit(uint64_t* bar, int leader) {
+    const uint16_t both = (uint16_t)(3 << leader);
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
                      smem_addr(bar)),
                  "h"(both)
                  : "memory");
 }
 
+// (bounded as if for more threads, so that a CTA of the first kernel finds registers on the SM: 128 or 96 each)
 template <bool Rows>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Rows ? 512 : kPairThreads, 1)
+__global__ void __launch_bounds__(Rows ? 512 : 640, 1)
     k_project_pair(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapX,
                    const __grid_constant__ CUtensorMap mapB, const __grid_constant__ CUtensorMap mapT, ProjectArgs a) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ PairSmem S;
     unsigned char* st = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     cg::cluster_group cl = cg::this_cluster();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = (int)cl.block_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ks = (int)cl.block_rank() >> 1, r = (int)cl.block_rank() & 1;
     const int half = a.bn / 2;
     const int stage_bytes = 2 * kPStageA + half * kPK * 2;
-    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+    const int first = blockIdx.x / (2 * a.split), step = a.split > 1 ? a.tiles : gridDim.x / 2;   // split: one tile per cluster
+    const int kb0 = (int)((int64_t)a.kblocks * ks / a.split), kb1 = (int)((int64_t)a.kblocks * (ks + 1) / a.split);
+    const int leader = 2 * ks;
     uint32_t* err = &g_project_err;
     auto stop = [&]() {   // a wait ran out: both CTAs of the pair end
         S.abort = 1;
-        *const_cast<volatile uint32_t*>(cl.map_shared_rank(const_cast<uint32_t*>(&S.abort), r ^ 1)) = 1;
+        *const_cast<volatile uint32_t*>(cl.map_shared_rank(const_cast<uint32_t*>(&S.abort), leader + (r ^ 1))) = 1;
     };
 
     if (tid == 0) {
@@ -760,10 +793,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Rows ? 512 : kPairTh
             };
             for (int tile = first; tile < a.tiles && !S.abort; tile += step) {
                 const int o0 = tile / a.row_tiles * (4 * kPM) + r * kPM, rt = tile % a.row_tiles, r0 = rt * a.bn + r * half;
-                for (int kb = 0; kb < a.kblocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     const int s = slot();
                     if (s < 0) break;
-                    const uint32_t p = smem_addr(st + s * stage_bytes), bar = map_rank0(smem_addr(&S.full[s]));
+                    const uint32_t p = smem_addr(st + s * stage_bytes), bar = map_rank(smem_addr(&S.full[s]), leader);
                     pair_load_2d(p, &mapW, kb * kPK, o0, bar);
                     pair_load_2d(p + kPStageA, &mapW, kb * kPK, o0 + 2 * kPM, bar);
                     pair_load_2d(p + 2 * kPStageA, &mapX, kb * kPK, r0, bar);
@@ -775,13 +808,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Rows ? 512 : kPairTh
                         waited = true;
                     }
                     const Entries entries{a.entry + rt * a.cap, S.ahead, __ldcg(a.counts + rt)};
-                    for (int j = 0; j < entries.count && !S.abort; ++j) {
-                        const int ad = entries.get(j, 0, 1);
+                    for (int j = ks; j < entries.count && !S.abort; j += a.split) {
+                        const int ad = entries.get(j, ks, a.split);
                         const int trow = (rt * a.cap + j) * a.bn + r * half;
                         for (int b = 0; b < per_entry; ++b) {
                             const int s = slot();
                             if (s < 0) break;
-                            const uint32_t p = smem_addr(st + s * stage_bytes), bar = map_rank0(smem_addr(&S.full[s]));
+                            const uint32_t p = smem_addr(st + s * stage_bytes), bar = map_rank(smem_addr(&S.full[s]), leader);
                             const int c = (b >> 1) * kPK, piece = b & 1;
                             pair_load_3d(p, &mapB, c, o0, ad, bar);
                             pair_load_3d(p + kPStageA, &mapB, c, o0 + 2 * kPM, ad, bar);
@@ -825,10 +858,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Rows ? 512 : kPairTh
                     return true;
                 };
                 auto next = [&]() {
-                    pair_commit(&S.empty[it % a.stages]);
+                    pair_commit(&S.empty[it % a.stages], leader);
                     ++it;
                 };
-                for (int kb = 0; kb < a.kblocks; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!block(kPK / 16, 0, false)) break;
                     next();
                 }
@@ -838,7 +871,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Rows ? 512 : kPairTh
                         waited = true;
                     }
                     const int count = __ldcg(a.counts + rt);
-                    for (int j = 0; j < count && !S.abort; ++j)
+                    for (int j = ks; j < count && !S.abort; j += a.split)
                         for (int b = 0; b < per_entry; ++b) {
                             if (one_block) {
                                 if (!block(R16 / 16, 0, false) || !block(R16 / 16, R16 / 16, true)) break;
@@ -848,7 +881,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Rows ? 512 : kPairTh
                             next();
                         }
                 }
-                pair_commit(&S.accF);
+                pair_commit(&S.accF, leader);
             }
         }
     } else if (warp >= 4) {
@@ -865,12 +898,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Rows ? 512 : kPairTh
             const bool ok = !S.abort;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + m * a.bn;
+            if (a.split > 1) break;   // the sums meet below
             store_tile<Rows>(a, taddr, o, lane, r0, rows, ok, acc);
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank0(smem_addr(&S.accE[m])))
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_addr(&S.accE[m]), leader))
                              : "memory");
+        }
+    }
+    if (a.split > 1) {
+        // the pairs' partial sums, one accumulator after the other through shared memory (its stages are done with),
+        // each pair finishes its share of the rows in pair order
+        const int r0 = first % a.row_tiles * a.bn, per = (a.bn + a.split - 1) / a.split;
+        const int c1 = min(min(a.bn, a.n - r0), per * (ks + 1));
+        for (int m = 0; m < 2; ++m) {
+            if (warp >= 4 && (warp - 4) >> 2 == m) {
+                const int qd = warp & 3;
+                const bool ok = !S.abort;
+                float* part = reinterpret_cast<float*>(st) + 32 * qd + lane;   // [bn][128]
+                const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + m * a.bn;
+                for (int c0 = 0; c0 < a.bn; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x16(taddr + c0, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(c0 + j) * kPM] = ok ? __uint_as_float(v[j]) : __int_as_float(0x7fffffff);
+                }
+            }
+            __syncwarp();
+            cl.sync();
+            finish_split(a, cl, reinterpret_cast<float*>(st), r, 2, first / a.row_tiles * (4 * kPM) + m * (2 * kPM) + r * kPM, r0,
+                         per * ks, c1, warp, kPairThreads / 32, lane);
+            cl.sync();   // the peers have read this CTA's sums
         }
     }
     if (Rows || a.counts) griddep_wait();
@@ -921,19 +981,25 @@ static cudaError_t encode(CUtensorMap* map, const void* base, uint64_t cols, uin
 static void project_tile(int n, int fin, int fout, ProjectWork& w) {
     constexpr int64_t n_sm = 148;   // the size of the work buffer must not depend on the current device
     const int64_t kb = (fin + kPK - 1) / kPK;
+    // clusters that run at once with one CTA per SM (a cluster lies in one GPC)
+    auto clusters = [](int64_t size) { return size <= 2 ? 74 : size <= 4 ? 33 : size <= 6 ? 22 : 15; };
     int64_t cost = INT64_MAX;
     const int widest = n <= 256 ? (n + 15) & ~15 : 256;
     for (int b = widest; b >= 16 && (b == widest || b >= 64); b -= 16) {
         const int64_t rows = (n + b - 1) / b, alone = rows * ((fout + kPM - 1) / kPM);
         for (int64_t split = 1; split <= 8; split *= 2) {
-            if (split > 1 && (alone * split > n_sm || kb < 4 * split)) break;
+            if (split > 1 && (alone > clusters(split) || kb < 4 * split)) break;
             const int64_t rounds = (alone + n_sm - 1) / n_sm;
             const int64_t c = rounds * ((kb + split - 1) / split * (kPM + b) * 128 / 33 + 5000) + (split > 1 ? 3000 + b * 8 : 0);
             if (c < cost) cost = c, w.bn = b, w.pair = false, w.split = (int)split;
         }
         const int64_t both = rows * ((fout + 4 * kPM - 1) / (4 * kPM)), rounds = (both + n_sm / 2 - 1) / (n_sm / 2);
-        const int64_t c = rounds * (kb * (2 * kPM + b / 2) * 128 / 33 + 8000 + b * 17);
-        if (c < cost) cost = c, w.bn = b, w.pair = true, w.split = 1;
+        for (int64_t split = 1; split <= 4; ++split) {
+            if (split > 1 && (n <= kRowsMax || both > clusters(2 * split) || kb < 4 * split)) break;
+            const int64_t c = rounds * ((kb + split - 1) / split * (2 * kPM + b / 2) * 128 / 33 + 8000 + b * 17) +
+                              (split > 1 ? 14000 + b * 24 : 0);
+            if (c < cost) cost = c, w.bn = b, w.pair = true, w.split = (int)split;
+        }
     }
 }
 
@@ -961,9 +1027,10 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     p.tiles = (p.fout + features - 1) / features * p.row_tiles;
     p.split = wk.split;
     const int stage = wk.pair ? 2 * kPStageA + p.bn / 2 * kPK * 2 : kPStageA + p.bn * kPK * 2;
-    // a decode batch with adapters leaves room for a CTA of the first kernel beside this one, so that W streams
-    // meanwhile (one row at 4096 x 4096: 14 us, without it 19)
-    const int t_bytes = p.rows ? p.n * p.rank * 4 : 0, room = p.rows || (p.counts && p.bn <= kRowsMax) ? kPSmemRows : kPSmem;
+    // with adapters, room for a CTA of the first kernel beside this one, so that W streams meanwhile (one row at
+    // 4096 x 4096: 14 us, without it 19)
+    const int t_bytes = p.rows ? p.n * p.rank * 4 : 0;
+    const int room = p.rows || (p.counts && p.bn <= kRowsMax) ? kPSmemRows : p.counts && p.rank <= 64 ? kPSmemEntries : kPSmem;
     p.stages = (room - t_bytes) / stage < kPMaxStages ? (room - t_bytes) / stage : kPMaxStages;
     const int smem = 1024 + p.stages * stage + t_bytes;   // the partial sums of a split tile (512 bytes per row) fit as well
 
@@ -1002,15 +1069,16 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     cudaLaunchConfig_t cfg = {};
     const int tiles_at_once = wk.pair ? n_sm / 2 : n_sm;
     const int tiles = p.split > 1 || p.tiles < tiles_at_once ? p.tiles : tiles_at_once;
-    cfg.gridDim = dim3((unsigned)(tiles * (wk.pair ? 2 : p.split)));
+    const int cluster = wk.pair ? 2 * p.split : p.split;
+    cfg.gridDim = dim3((unsigned)(tiles * cluster));
     cfg.blockDim = dim3(wk.pair ? kPairThreads : kPThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     unsigned na = 0;
-    if (p.split > 1) {
+    if (cluster > 1) {
         at[na].id = cudaLaunchAttributeClusterDimension;
-        at[na].val.clusterDim.x = (unsigned)p.split;
+        at[na].val.clusterDim.x = (unsigned)cluster;
         at[na].val.clusterDim.y = at[na].val.clusterDim.z = 1;
         ++na;
     }
