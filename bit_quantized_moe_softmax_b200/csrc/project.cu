@@ -98,7 +98,7 @@ template <int NT, int kShRows>   // 8-wide rank blocks; rows per item
 __global__ void __launch_bounds__(NT == 8 ? 320 : 256, NT >= 8 ? 2 : NT == 4 ? 4 : 5) k_adapter_shrink(ShrinkArgs a) {
     extern __shared__ __align__(128) unsigned char ring[];   // [kShStages][kShRows + 8 NT rows][128 bytes]
     __shared__ __align__(16) int s_id[256];
-    __shared__ int s_w[8], s_rank[256], s_adapter[256], s_n[256], s_rows[kShRows], s_j, s_c0, s_cnt;
+    __shared__ int s_w[8], s_key[512], s_lead[512], s_rank[256], s_adapter[256], s_n[256], s_rows[kShRows], s_j, s_c0, s_cnt;
     constexpr int kStageRows = kShRows + 8 * NT;
     griddep_launch();   // the projection may start on W; it waits for this grid before it reads t
     cg::cluster_group cl = cg::this_cluster();
@@ -112,15 +112,20 @@ __global__ void __launch_bounds__(NT == 8 ? 320 : 256, NT >= 8 ? 2 : NT == 4 ? 4
     const int id = (unsigned)row_id < (unsigned)a.n_adapters ? row_id : -1;   // any other id: no adapter
     s_id[tid] = id;
     s_n[tid] = 0;
+    s_key[tid] = s_key[tid + 256] = -1;
+    s_lead[tid] = s_lead[tid + 256] = 256;
     __syncthreads();
-    int lead = tid;   // the first row with this id
+    int slot = id & 511;   // a hash table of at most 256 adapters: each one's first row
     if (id >= 0) {
-        for (int k = 0; k < tid; k += 4) {
-            const int4 v = *reinterpret_cast<const int4*>(s_id + k);
-            const int f = v.x == id ? k : v.y == id ? k + 1 : v.z == id ? k + 2 : v.w == id ? k + 3 : 256;
-            lead = min(lead, f);
+        for (;;) {
+            const int old = atomicCAS(&s_key[slot], -1, id);
+            if (old == -1 || old == id) break;
+            slot = (slot + 1) & 511;
         }
+        atomicMin(&s_lead[slot], tid);
     }
+    __syncthreads();
+    const int lead = id >= 0 ? s_lead[slot] : tid;
     auto scan = [&](int v, int& before) {   // exclusive prefix over the threads, and the total
         int inc = v;
 #pragma unroll
@@ -1045,12 +1050,13 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     if (p.counts || p.rows) {
         s.bn = p.bn;
         s.cap = p.cap;
-        // CTAs per item: each at least four column blocks; eight for a few rows, which leave SMs idle
+        // CTAs per item: each at least four column blocks; eight where the items leave SMs idle
+        const int items = p.cap + p.bn / (p.rows ? 16 : 64);   // at most, per tile
         s.split = 1;
-        const int most = s.n <= 16 ? 8 : 4;
+        const int most = items * p.row_tiles * 8 <= 2 * n_sm ? 8 : 4;
         while (s.split < most && p.kblocks >= 8 * s.split) s.split *= 2;
         // clusters per tile: as many as it can have items, or as fill the SMs about four times over
-        const int items = p.cap + p.bn / (p.rows ? 16 : 64), fill = 4 * n_sm / (s.split * p.row_tiles);
+        const int fill = 4 * n_sm / (s.split * p.row_tiles);
         const int y = items < fill ? items : fill < 4 ? 4 : fill;
         const dim3 grid(s.split, y, p.row_tiles);
         const int nt = (p.rank + 7) / 8;
