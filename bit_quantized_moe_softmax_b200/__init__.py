@@ -431,8 +431,13 @@ def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch
                                ("ids", ids, (n,), (torch.int32,))))
     if na and n:
         if work is None:
-            work = torch.empty(lib().ds4moe_project_work_bytes(n, fin, fout, na, rank), dtype=torch.uint8,
-                               device=x.device)
+            # of the stream that the call runs on: the allocator then hands it on only behind the call
+            need = lib().ds4moe_project_work_bytes(n, fin, fout, na, rank)
+            if stream is None:
+                work = torch.empty(need, dtype=torch.uint8, device=x.device)
+            else:
+                with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=x.device)):
+                    work = torch.empty(need, dtype=torch.uint8, device=x.device)
         elif work.get_device() != dev or not work.is_contiguous():
             _refuse(where, "work: contiguous on %s expected" % x.device)
         wb = work.numel() * work.element_size()

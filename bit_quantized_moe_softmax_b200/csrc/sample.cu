@@ -317,6 +317,11 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
         for (int i = tid; i < kSW * a.seg; i += kST) vals[i] = vals[i] == INFINITY ? 0.f : kNegInf;
         mx = 0.f;
         __syncthreads();
+    } else if (mx > 1e37f) {   // no difference of logits may overflow: everything by 2^-8
+        for (int i = tid; i < kSW * a.seg; i += kST) vals[i] *= 0.00390625f;
+        mx *= 0.00390625f;
+        T *= 0.00390625f;
+        __syncthreads();
     }
     const bool by_k = K >= 1 && K < a.V, by_p = P < 1.f, by_m = mp > 0.f;
     const double minw = fmin((double)mp, 1.0);

@@ -258,7 +258,9 @@ ds4moe_status ds4moe_widen_rows(const void* d_q, int32_t q_format, const float* 
  * enters the second product with 16 bits.  d_x [n][in], d_W [out][in], d_A
  * [n_adapters][rank][in], d_B [n_adapters][out][rank], d_scale [n_adapters]
  * binary32, d_ids [n] int32: an id outside 0 .. n_adapters-1 (-1, say) means
- * no adapter.  n_adapters 0: the projection alone (the adapter arguments and
+ * no adapter.  The adapters' values have to be finite: an infinity or NaN in
+ * one's B may reach that output of other rows (values of x reach their own row
+ * alone).  n_adapters 0: the projection alone (the adapter arguments and
  * the work buffer are ignored).  Rows may come in any order; rows of one
  * adapter next to each other are fastest (the cost of the adapters goes by the
  * distinct ones among a tile's rows).  in a multiple of 8 up to 65536, out

@@ -171,6 +171,20 @@ def test_stream_graph_and_work_buffer():
         m.ds4moe_project(out=out, work=work[:64], **d)
 
 
+def test_own_work_buffers_of_several_streams():
+    """Calls without a work buffer on two side streams and the current one, in turn: each has its own."""
+    ds = [_data(n, 512, 640, 7, 16, seed=n) for n in (3, 48, 100)]
+    refs = [_check(d) for d in ds]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), None]
+    outs = [[torch.empty_like(r) for _ in range(12)] for r in refs]
+    torch.cuda.synchronize()
+    for i in range(12):
+        for d, o, s in zip(ds, outs, streams):
+            m.ds4moe_project(out=o[i], stream=s, **d)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, r) for os_, r in zip(outs, refs) for o in os_)
+
+
 def test_refuses_overlaps_and_layouts():
     d = _data(8, 64, 64, 0, 0)
     with pytest.raises(m.Ds4MoeError):

@@ -182,6 +182,17 @@ def test_masked_and_broken_logits(V):
     _check(l.to(BF16), u, k=4, p=0.9)
 
 
+@pytest.mark.parametrize("T", [1.0, 1e36, 3e38, INF])
+def test_logits_over_the_whole_range(T):
+    """Differences of logits beyond binary32's largest value."""
+    l, u = _logits(4, 3000)
+    l *= 1e37
+    l[:, 7] = 3.3e38
+    l[:, 11::5] = torch.finfo(F32).min
+    for f in (dict(), dict(k=9), dict(p=0.5), dict(k=2000, p=0.9, mp=0.01)):
+        _check(l, u, T=T, **f)
+
+
 @pytest.mark.parametrize("dtype, pad, start", [(F32, 0, 1), (F32, 3, 2), (BF16, 5, 0), (BF16, 8, 1), (BF16, 1, 3)])
 def test_strided_and_unaligned_rows(dtype, pad, start):
     V = 5000
