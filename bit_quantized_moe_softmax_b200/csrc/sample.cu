@@ -47,7 +47,7 @@ constexpr u64 kOffset = 0x4338000000000000ull;   // kMagic's bits
 struct __align__(16) SampleSmem {
     uint32_t hist[2][2][kBins];      // two in turn: counts in the first array, or the low and high words of weights
     u64 group[2][kMaxCluster][32];   // sums of 64 bins of each CTA, written by the peers; two in turn
-    u64 list[kList];                 // this CTA's tokens of a bin (the first kList / C), then all of them in order
+    u64 list[kList];                 // this CTA's tokens of a bin, then all of them in order
     uint32_t listed[kMaxCluster];    // how many there are in each CTA
     uint32_t list_n;
     double tab[kTab];
@@ -80,16 +80,29 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(
 struct Weigh {
     double M, c;           // c = 128 log2(e) / T, at most where one step below M already weighs nothing
     float Mf, cf;
-    float low;             // M - 8192 / c
+    double reach;          // 8192 / c
+    float low;             // M - reach
     bool flat;             // T so large that low is the lowest binary32 value: -infinity is tested for
     const double* tab;
 
-    __device__ void set(float m, float T, const double* table) {
+    // before the row's maximum is known
+    __device__ __forceinline__ void set_temperature(float T, const double* table) {
+        c = fmin(kTab * 1.44269504088896340736 / (double)T, 1e38);
+        reach = fmax(8192.0 / (kTab * 1.44269504088896340736) * (double)T, 8192e-38);   // 8192 / c
+        tab = table;
+    }
+    // the maximum; everything scaled by 2^-shift
+    __device__ __forceinline__ void set_maximum(float m, int shift) {
+        const double by = __hiloint2double((1023 + shift) << 20, 0);
+        c = fmin(c * by, 1e38), reach /= by;
         const float below = __uint_as_float(m > 0.f ? __float_as_uint(m) - 1 : m < 0.f ? __float_as_uint(m) + 1 : 0x80000001u);
-        M = m, Mf = m, tab = table;
-        c = fmin(fmin(kTab * 1.44269504088896340736 / (double)T, 6000.0 / ((double)m - (double)below)), 1e38);
+        // a power of two (2^104 at the lowest value), and 1 / step by its exponent
+        const double step = below == kNegInf ? 0x1p104 : (double)m - (double)below;
+        const double most = 6000.0 * __hiloint2double(0x7fe00000 - __double2hiint(step), 0);
+        if (c > most) c = most, reach = 8192.0 / 6000.0 * step;
+        M = m, Mf = m;
         cf = (float)c;
-        const double l = (double)m - 8192.0 / c;   // (c = 0: -infinity)
+        const double l = (double)m - reach;
         flat = !(l > -3.4e38);
         low = flat ? -3.402823466e38f : __double2float_rd(l);
     }
@@ -204,6 +217,12 @@ __device__ __noinline__ void find_bin(SampleSmem& S, int buf, bool wide, u64 tar
     __syncthreads();   // part is free again
 }
 
+// The sum that the running sum has to exceed: u of the total, the last unit at most.
+__device__ __forceinline__ u64 draw_target(float u, u64 total) {
+    const double x = (double)u * (double)total;
+    return !(x > 0.0) ? 0 : x >= (double)total ? total - 1 : min((u64)x, total - 1);
+}
+
 // A token in the order of the filters, largest first: key, then the lower index.
 __device__ __forceinline__ u64 order_of(uint32_t key, int idx) { return ((u64)key << 32) | (uint32_t)~idx; }
 
@@ -247,6 +266,11 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
     float P = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
     if (!(T > 0.f)) T = 1.f, K = 1, P = 1.f, mp = 0.f, u = 0.f;   // greedy: the first token of the order
 
+    const double inv = 1.0 / (double)T;
+    Weigh weigh;
+    weigh.set_temperature(T, S.tab);
+    int shift = 0;
+
     // ---- the row into shared memory, and its maximum; a NaN counts as -infinity
     float mx = kNegInf;
     auto clean = [&](float v) {
@@ -288,7 +312,14 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
         }
         for (int i = cnt + tid; i < kSW * a.seg; i += kST) vals[i] = kNegInf;
     }
-    if (tid < kTab) S.tab[tid] = exp2((double)tid / kTab);
+    if (tid < kTab) {   // 2^(tid / 128) from the powers of its bits
+        const double power[7] = {1.0054299011128027, 1.0108892860517005, 1.0218971486541166, 1.0442737824274138,
+                                 1.0905077326652577, 1.189207115002721,  1.4142135623730951};
+        double w = 1.0;
+#pragma unroll
+        for (int b = 0; b < 7; ++b) w *= tid >> b & 1 ? power[b] : 1.0;
+        S.tab[tid] = w;
+    }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, m));
     if (lane == 0) S.wmax[warp] = mx;
@@ -320,14 +351,12 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
     } else if (mx > 1e37f) {   // no difference of logits may overflow: everything by 2^-8
         for (int i = tid; i < kSW * a.seg; i += kST) vals[i] *= 0.00390625f;
         mx *= 0.00390625f;
-        T *= 0.00390625f;
+        shift = 8;
         __syncthreads();
     }
     const bool by_k = K >= 1 && K < a.V, by_p = P < 1.f, by_m = mp > 0.f;
     const double minw = fmin((double)mp, 1.0);
-    const double inv = 1.0 / (double)T;
-    Weigh weigh;
-    weigh.set(mx, T, S.tab);
+    weigh.set_maximum(mx, shift);
     const int s0 = warp * a.seg;   // this warp's tokens: s0 .. s0 + seg - 1
 
     // ---- the prefix that top-k and top-p keep: tokens above thr, and those at it up to index last of the row
@@ -343,16 +372,59 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
         }
     };
     int buf = 0;
+    // Top-k of at most kList tokens: they are in order, one per thread, so that top-p, min-p and the draw need no
+    // more passes over the row.
+    bool small = false;
+    u64 small_total = 0;
+    auto scan = [&](u64 w) {   // inclusive sums over the CTA's threads
+        u64 inc = warp_scan(w, lane);
+        __syncthreads();
+        if (lane == 31) S.wsum[warp] = inc;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kSW; ++x)
+            if (x < warp) inc += S.wsum[x];
+        return inc;
+    };
+    auto kept_few = [&](u64 v) {
+        const float l = key_value((uint32_t)(v >> 32));
+        const double w = weigh(l);
+        const u64 units = v && tid < K ? Weigh::to_units(w) : 0, inc = scan(units);
+        if (tid == K - 1) S.list[0] = inc;
+        __syncthreads();
+        u64 target = S.list[0];   // top-k's total
+        if (by_p) target = min(target, max(1ull, (u64)__double2ll_ru(fmax((double)P, 0.0) * (double)target)));
+        // (what follows the last token with a weight is not in: the first one always is)
+        const bool in = units && inc - units < target && (tid == 0 || !(by_m && w < minw));
+        const int m = __syncthreads_count(in);   // a prefix
+        if (tid == m - 1) S.list[0] = v, S.list[1] = inc;
+        __syncthreads();
+        thr = key_value((uint32_t)(S.list[0] >> 32));
+        last = (int)~(uint32_t)S.list[0];
+        small_total = S.list[1];
+        __syncthreads();
+        if (r != 0) return;
+        // the draw goes by index: the same tokens in that order, their keys beside
+        const u64 by_index = sort_desc(S, tid < m ? ((u64)(uint32_t)v << 32) | (v >> 32) : 0);
+        const float li = key_value((uint32_t)by_index);
+        const double wi = weigh(li);
+        const u64 ui = by_index ? Weigh::to_units(wi) : 0, run = scan(ui);
+        const u64 at = draw_target(u, small_total);
+        if (ui && at < run && at >= run - ui) {   // one thread
+            a.token[row] = (int)~(uint32_t)(by_index >> 32);
+            if (a.prob) a.prob[row] = (float)(wi * (kOne / (double)small_total));
+        }
+    };
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         const bool mass = pass == 1;
-        if (!(mass ? by_p : by_k)) continue;
+        if (!(mass ? by_p : by_k) || small) continue;
         // steps of 1/128 of a temperature for masses, of 1/64 for counts: a few hundred tokens at most in the
         // bins that matter
-        const Coarse coarse{mx, (float)fmin(fmax(mass ? inv * 128.0 : 64.0, 1e-38), 1e38)};
+        const Coarse coarse{mx, (float)fmin(fmax(mass ? inv * (shift ? 32768.0 : 128.0) : 64.0, 1e-38), 1e38)};
         u64 target = (u64)K, before = 0, own = 0;
         uint32_t bin = 0, lo = 0, hi = 0;
-        bool found = false;
+        bool found = false, few = false;
         // The first histogram; if its bin holds too many tokens to order at once, the bits of the keys in it.
 #pragma unroll 1
         for (int round = 0;; ++round) {
@@ -427,14 +499,17 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
             before += rel;
             found = true;
             if (round == 0) {
-                // the tokens of the bin: a list of the first few, and the range of their keys
+                // the tokens of the bin: a list of the first few, and the range of their keys; where top-k leaves
+                // few tokens, of the bins above too
                 bin = b;
+                few = !mass && before + own <= kList;
                 uint32_t l0 = 0xffffffffu, h0 = 0;
                 each([&](const float (&l)[4], int i) {
                     bool in[4], any = false;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        in[e] = coarse(l[e]) == bin && l[e] > kNegInf;
+                        const uint32_t b = coarse(l[e]);
+                        in[e] = (few ? b <= bin : b == bin) && l[e] > kNegInf;
                         any |= in[e];
                     }
                     if (!__any_sync(kAll, any)) return;
@@ -444,7 +519,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                             const uint32_t k = order_key(l[e]);
                             l0 = min(l0, k), h0 = max(h0, k);
                             const uint32_t at = atomicAdd(&S.list_n, 1u);   // any order: they are sorted
-                            if (at < kList / C) S.list[at] = order_of(k, begin + i + e);
+                            if (at < kList) S.list[at] = order_of(k, begin + i + e);
                         }
                     }
                 });
@@ -460,19 +535,27 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                     cl.map_shared_rank(S.listed, tid)[r] = S.list_n;
                 }
                 cl.sync();
-                bool fits = true;
+                uint32_t listed = 0;
+                int from = 0, j = tid;   // this thread's token: the j-th of CTA from
 #pragma unroll
                 for (int p = 0; p < C; ++p) {
+                    const uint32_t n = S.listed[p];
                     l0 = min(l0, S.klo[p]), h0 = max(h0, S.khi[p]);
-                    fits &= S.listed[p] <= kList / C;
+                    if (tid >= listed + n) from = p + 1, j = (int)(tid - listed - n);
+                    listed += n;
                 }
                 lo = l0, hi = h0;
-                if (fits) {
-                    const int p = tid / (kList / C), j = tid % (kList / C);
-                    u64 v = (uint32_t)j < S.listed[p] ? cl.map_shared_rank(S.list, p)[j] : 0;
+                if (listed <= kList) {
+                    u64 v = (uint32_t)tid < listed ? cl.map_shared_rank(S.list, from)[j] : 0;
                     if (C > 1) cl.sync();   // the peers have read this CTA's list
                     else __syncthreads();
                     v = sort_desc(S, v);
+                    if (few) {
+                        small = true;
+                        kept_few(v);
+                        found = false;
+                        break;
+                    }
                     const float l = key_value((uint32_t)(v >> 32));
                     const u64 w = !v ? 0 : mass ? weigh.units(l) : 1;
                     u64 inc = warp_scan(w, lane);
@@ -540,7 +623,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
             }
             thr = at;
         }
-        if (!mass && by_p) {   // what top-k removes is gone for top-p
+        if (!mass && by_p && !small) {   // what top-k removes is gone for top-p
             each([&](const float (&l)[4], int i) {
                 if (!__any_sync(kAll, l[0] > kNegInf || l[1] > kNegInf || l[2] > kNegInf || l[3] > kNegInf)) return;
                 float4 v;
@@ -575,8 +658,9 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
     };
 
     // ---- their total, and each warp's share
-    u64 sum = 0;
-    if (by_k || by_p) {
+    u64 total = small_total, base = 0, sum = 0;
+    if (small) {
+    } else if (by_k || by_p) {
         // few of many, as a rule: the warp gathers them and takes the exponentials of 32 at a time
         // (in the histogram that was not the last: its peers' reads ended before a barrier)
         float* queue = reinterpret_cast<float*>(S.hist[buf]) + warp * 160;
@@ -629,33 +713,34 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
         }
         sum -= (u64)(a.seg / 32) * kOffset;   // seg / 32 tokens a lane
     }
-    sum = warp_sum(sum);
-    __syncthreads();   // S.wsum of find_bin has been read
-    if (lane == 0) S.wsum[warp] = sum;
-    __syncthreads();
-    u64 base = 0, all = 0;
+    if (!small) {
+        sum = warp_sum(sum);
+        __syncthreads();   // S.wsum of the threshold has been read
+        if (lane == 0) S.wsum[warp] = sum;
+        __syncthreads();
+        u64 all = 0;
 #pragma unroll
-    for (int w = 0; w < kSW; ++w) {
-        if (w < warp) base += S.wsum[w];
-        all += S.wsum[w];
-    }
-    u64 total = all;
-    if (C > 1) {
-        if (tid < C) cl.map_shared_rank(S.slice_tot, tid)[r] = all;
-        cl.sync();
-        total = 0;
+        for (int w = 0; w < kSW; ++w) {
+            if (w < warp) base += S.wsum[w];
+            all += S.wsum[w];
+        }
+        total = all;
+        if (C > 1) {
+            if (tid < C) cl.map_shared_rank(S.slice_tot, tid)[r] = all;
+            cl.sync();
+            total = 0;
 #pragma unroll
-        for (int p = 0; p < C; ++p) {
-            if (p < r) base += S.slice_tot[p];
-            total += S.slice_tot[p];
+            for (int p = 0; p < C; ++p) {
+                if (p < r) base += S.slice_tot[p];
+                total += S.slice_tot[p];
+            }
         }
     }
     const double norm = kOne / (double)total;
 
     // ---- the draw: the first kept token whose running sum exceeds u of the total
-    const double x = (double)u * (double)total;
-    const u64 target = !(x > 0.0) ? 0 : x >= (double)total ? total - 1 : min((u64)x, total - 1);
-    if (target >= base && target < base + sum) {   // one warp of the cluster
+    const u64 target = draw_target(u, total);
+    if (!small && target >= base && target < base + sum) {   // one warp of the cluster
         u64 run = base;
         for (int i = s0 + 4 * lane; i < s0 + a.seg; i += 128) {
             double w[4];

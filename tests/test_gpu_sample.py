@@ -182,6 +182,16 @@ def test_masked_and_broken_logits(V):
     _check(l.to(BF16), u, k=4, p=0.9)
 
 
+@pytest.mark.parametrize("k", [63, 64, 500, 511, 512, 513, 700])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_top_k_about_a_ctas_threads(k, dtype):
+    """Where the kept tokens stop fitting one per thread; bf16's ties put many at the threshold."""
+    for V in (1000, 30000, 140000):
+        l, u = _logits(2, V, dtype, seed=k)
+        for f in (dict(k=k), dict(k=k, p=0.97), dict(k=k, T=0.3, mp=0.1), dict(k=k, T=3.0, p=0.5)):
+            _check(l, u, **f)
+
+
 @pytest.mark.parametrize("T", [1.0, 1e36, 3e38, INF])
 def test_logits_over_the_whole_range(T):
     """Differences of logits beyond binary32's largest value."""
