@@ -3,11 +3,12 @@
 //
 // Two kernels.  k_adapter_shrink computes t_i = s_a A_a x_i for every row with
 // an adapter and writes it as two bf16 pieces (hi, lo = t - hi: 16 bits, half
-// a unit of 2^-17 next to bf16's 2^-9 in y).  k_project is one tcgen05 GEMM
-// whose K axis runs on past W: for every adapter a found among a tile's rows
-// it has further K blocks [B_a] x [t of a's rows, zero in the others].  The
-// adapters so cost a few K steps of the same accumulation and y is written
-// once, with one rounding.
+// a unit of 2^-17 next to bf16's 2^-9 in y).  k_project (k_project_pair) is one
+// tcgen05 GEMM whose K axis runs on past W: for every adapter a found among a
+// tile's rows it has further K blocks [B_a] x [t of a's rows, zero in the
+// others].  The adapters so cost a few K steps of the same accumulation and y is
+// written once, with one rounding.  For 8 to 64 rows the second product is
+// outside the MMAs instead (adapter_rows).
 //
 // The weights are the M side of the MMA (128 output features per tile) and the
 // rows the N side (16 to 256), so that one row costs a sixteenth of a tile's
@@ -74,9 +75,9 @@ __host__ __device__ inline int t_cols(int rank) { return 2 * ((rank + 15) & ~15)
 // ---------------------------------------------------------------- t = s A x, by (row tile, adapter)
 // Workspace: counts [tiles], adapter of each entry [tiles][cap], then t
 // [tiles][cap][bn][t_cols].  Entry j of a tile is its j-th distinct adapter in
-// order of first appearance.
+// order of first appearance.  For 8 to 64 rows t alone, in binary32: [n][rank].
 //
-// A cluster of `split` CTAs takes up to 64 rows of one adapter in one tile, each
+// A cluster of `split` CTAs takes up to 64 rows (16 there) of one adapter, each
 // CTA a part of the input columns: 64-column blocks of the rows and of A go
 // through a ring of shared-memory stages (cp.async, 16-byte units swizzled by
 // row), the rows are the M side of mma.sync m16n8k16, the rank the N side, and
