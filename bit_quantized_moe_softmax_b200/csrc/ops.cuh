@@ -27,6 +27,7 @@ struct AddNormArgs {
     int out_bf16;
     float eps, qmax;
     int warps_per_row;    // set by the launcher
+    double inv_H;
 };
 cudaError_t launch_add_rmsnorm(AddNormArgs a, bool x_bf16, int res_kind, bool vec, int n_sm, cudaStream_t st);
 

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(CH == 4 ? 512 : 1024) k_add_rmsnorm(AddNormArg
         acc = 0.0;
         for (int i = 0; i < nw; ++i) acc += s_sum[i];
     }
-    const float rstd = (float)(1.0 / sqrt(acc / (double)H + (double)a.eps));
+    const float rstd = (float)rsqrt(fma(acc, a.inv_H, (double)a.eps));
 
     // y in place of s; the largest magnitude as its bit pattern (a NaN's is above infinity's, so it stays)
     uint32_t mx = 0;
@@ -284,6 +284,7 @@ cudaError_t launch_add_rmsnorm(AddNormArgs a, bool x_bf16, int res_kind, bool ve
     int ch = blocks > 32 ? 4 : a.n < 2 * n_sm ? 1 : 2;
     if (blocks < ch) ch = 1;
     a.warps_per_row = (blocks + ch - 1) / ch;
+    a.inv_H = 1.0 / (double)a.H;
     const bool solo = a.warps_per_row == 1;
     const int rows_per_cta = solo ? 4 : 1;
     const dim3 block(32 * (solo ? rows_per_cta : a.warps_per_row));
