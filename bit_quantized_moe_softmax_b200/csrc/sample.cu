@@ -372,8 +372,8 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
         }
     };
     int buf = 0;
-    // Top-k of at most kList tokens: they are in order, one per thread, so that top-p, min-p and the draw need no
-    // more passes over the row.
+    // At most kList tokens that top-k or top-p may keep: they are in order, one per thread, so that the filters that
+    // are left and the draw need no more passes over the row.
     bool small = false;
     u64 small_total = 0;
     auto scan = [&](u64 w) {   // inclusive sums over the CTA's threads
@@ -386,14 +386,18 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
             if (x < warp) inc += S.wsum[x];
         return inc;
     };
-    auto kept_few = [&](u64 v) {
+    // v: this thread's token; the first n count; target: top-p's, or 0 for top-k
+    auto kept_few = [&](u64 v, int n, u64 target) {
         const float l = key_value((uint32_t)(v >> 32));
         const double w = weigh(l);
-        const u64 units = v && tid < K ? Weigh::to_units(w) : 0, inc = scan(units);
-        if (tid == K - 1) S.list[0] = inc;
-        __syncthreads();
-        u64 target = S.list[0];   // top-k's total
-        if (by_p) target = min(target, max(1ull, (u64)__double2ll_ru(fmax((double)P, 0.0) * (double)target)));
+        const u64 units = v && tid < n ? Weigh::to_units(w) : 0, inc = scan(units);
+        if (!target) {
+            if (tid == n - 1) S.list[0] = inc;
+            __syncthreads();
+            target = S.list[0];   // top-k's total
+            if (by_p) target = min(target, max(1ull, (u64)__double2ll_ru(fmax((double)P, 0.0) * (double)target)));
+            __syncthreads();
+        }
         // (what follows the last token with a weight is not in: the first one always is)
         const bool in = units && inc - units < target && (tid == 0 || !(by_m && w < minw));
         const int m = __syncthreads_count(in);   // a prefix
@@ -502,8 +506,12 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                 // the tokens of the bin: a list of the first few, and the range of their keys; where top-k leaves
                 // few tokens, of the bins above too
                 bin = b;
-                few = !mass && before + own <= kList;
-                uint32_t l0 = 0xffffffffu, h0 = 0;
+                // (a mass: each of its tokens weighs more than one a step below the bin)
+                few = before + own <= (mass ? kList * weigh.units(mx - ((float)bin + 1.f) / coarse.step) : (u64)kList);
+                uint32_t l0, h0, listed;
+                int from, j;
+            list:
+                l0 = 0xffffffffu, h0 = 0;
                 each([&](const float (&l)[4], int i) {
                     bool in[4], any = false;
 #pragma unroll
@@ -535,14 +543,21 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                     cl.map_shared_rank(S.listed, tid)[r] = S.list_n;
                 }
                 cl.sync();
-                uint32_t listed = 0;
-                int from = 0, j = tid;   // this thread's token: the j-th of CTA from
+                listed = 0, from = 0, j = tid;   // this thread's token: the j-th of CTA from
 #pragma unroll
                 for (int p = 0; p < C; ++p) {
                     const uint32_t n = S.listed[p];
                     l0 = min(l0, S.klo[p]), h0 = max(h0, S.khi[p]);
                     if (tid >= listed + n) from = p + 1, j = (int)(tid - listed - n);
                     listed += n;
+                }
+                if (few && listed > kList) {   // (a bound missed by a rounding)
+                    few = false;
+                    if (C > 1) cl.sync();
+                    __syncthreads();
+                    if (tid == 0) S.list_n = 0;
+                    __syncthreads();
+                    goto list;
                 }
                 lo = l0, hi = h0;
                 if (listed <= kList) {
@@ -552,7 +567,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                     v = sort_desc(S, v);
                     if (few) {
                         small = true;
-                        kept_few(v);
+                        kept_few(v, mass ? kList : K, mass ? target : 0);
                         found = false;
                         break;
                     }

@@ -192,6 +192,17 @@ def test_top_k_about_a_ctas_threads(k, dtype):
             _check(l, u, **f)
 
 
+@pytest.mark.parametrize("spread", [0.01, 1.0, 4.0, 12.0])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_nuclei_of_all_sizes(spread, dtype):
+    """Flat and peaked rows: top-p keeps from one token to nearly all of them."""
+    for V in (700, 25000, 131072):
+        l, u = _logits(3, V, dtype, spread=spread, seed=int(10 * spread))
+        for p in (0.05, 0.5, 0.9, 0.999):
+            _check(l, u, p=p)
+            _check(l, u, p=p, k=2000, mp=0.003, probs=False)
+
+
 @pytest.mark.parametrize("T", [1.0, 1e36, 3e38, INF])
 def test_logits_over_the_whole_range(T):
     """Differences of logits beyond binary32's largest value."""
