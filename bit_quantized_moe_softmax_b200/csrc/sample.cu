@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
         for (int b = 0; b < 7; ++b) w *= tid >> b & 1 ? power[b] : 1.0;
         S.tab[tid] = w;
     }
+    float own_max = mx;   // of the tokens that this thread brought
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, m));
     if (lane == 0) S.wmax[warp] = mx;
@@ -347,10 +348,12 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
     if (mx == INFINITY) {   // the tokens there share all the weight
         for (int i = tid; i < kSW * a.seg; i += kST) vals[i] = vals[i] == INFINITY ? 0.f : kNegInf;
         mx = 0.f;
+        own_max = own_max == INFINITY ? 0.f : kNegInf;
         __syncthreads();
     } else if (mx > 1e37f) {   // no difference of logits may overflow: everything by 2^-8
         for (int i = tid; i < kSW * a.seg; i += kST) vals[i] *= 0.00390625f;
         mx *= 0.00390625f;
+        own_max *= 0.00390625f;
         shift = 8;
         __syncthreads();
     }
@@ -429,6 +432,9 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
         u64 target = (u64)K, before = 0, own = 0;
         uint32_t bin = 0, lo = 0, hi = 0;
         bool found = false, few = false;
+        // Top-k of a few: k threads' largest tokens bound the k-th token from below, and a histogram of those is
+        // enough to list little more than k tokens.
+        bool probe = !mass && K <= C * kST / 4;
         // The first histogram; if its bin holds too many tokens to order at once, the bits of the keys in it.
 #pragma unroll 1
         for (int round = 0;; ++round) {
@@ -443,7 +449,9 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                 const uint32_t y = (uint32_t)(v >> 32) + (old + x < x);   // with the carry
                 if (y) atomicAdd(&S.hist[buf][1][b], y);
             };
-            if (round == 0) {
+            if (probe) {
+                if (own_max > kNegInf) atomicAdd(&S.hist[buf][0][coarse(own_max)], 1u);
+            } else if (round == 0) {
                 each([&](const float (&l)[4], int) {
                     // (after top-k most steps hold nothing)
                     if (!__any_sync(kAll, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) > kNegInf)) return;
@@ -493,7 +501,9 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                     target = min(target, total);
                 } else if (total < target) {   // top-k of more tokens than there are
                     buf ^= 1;
-                    break;
+                    if (!probe) break;
+                    probe = false, round = -1;
+                    continue;
                 }
             }
             uint32_t b;
@@ -507,28 +517,36 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                 // few tokens, of the bins above too
                 bin = b;
                 // (a mass: each of its tokens weighs more than one a step below the bin)
-                few = before + own <= (mass ? kList * weigh.units(mx - ((float)bin + 1.f) / coarse.step) : (u64)kList);
+                const float lowest = -3.402823466e38f;
+                const float edge = bin == kBins - 1 ? lowest : fmaxf(mx - ((float)bin + 1.f) / coarse.step, lowest);
+                few = probe || before + own <= (mass ? kList * weigh.units(edge) : (u64)kList);
                 uint32_t l0, h0, listed;
                 int from, j;
             list:
                 l0 = 0xffffffffu, h0 = 0;
+                auto list = [&](float l, int i) {
+                    const uint32_t k = order_key(l);
+                    l0 = min(l0, k), h0 = max(h0, k);
+                    const uint32_t at = atomicAdd(&S.list_n, 1u);   // any order: they are sorted
+                    if (at < kList) S.list[at] = order_of(k, begin + i);
+                };
                 each([&](const float (&l)[4], int i) {
-                    bool in[4], any = false;
+                    if (few) {   // all down to the bin's end, and perhaps one or two more
+                        if (!__any_sync(kAll, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= edge)) return;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t b = coarse(l[e]);
-                        in[e] = (few ? b <= bin : b == bin) && l[e] > kNegInf;
-                        any |= in[e];
-                    }
-                    if (!__any_sync(kAll, any)) return;
+                        for (int e = 0; e < 4; ++e)
+                            if (l[e] >= edge) list(l[e], i + e);
+                    } else {
+                        bool in[4], any = false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (in[e]) {
-                            const uint32_t k = order_key(l[e]);
-                            l0 = min(l0, k), h0 = max(h0, k);
-                            const uint32_t at = atomicAdd(&S.list_n, 1u);   // any order: they are sorted
-                            if (at < kList) S.list[at] = order_of(k, begin + i + e);
+                        for (int e = 0; e < 4; ++e) {
+                            in[e] = coarse(l[e]) == bin && l[e] > kNegInf;
+                            any |= in[e];
                         }
+                        if (!__any_sync(kAll, any)) return;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (in[e]) list(l[e], i + e);
                     }
                 });
                 l0 = __reduce_min_sync(kAll, l0);
@@ -550,6 +568,10 @@ __global__ void __launch_bounds__(kST, 2) k_sample(SampleArgs a) {
                     l0 = min(l0, S.klo[p]), h0 = max(h0, S.khi[p]);
                     if (tid >= listed + n) from = p + 1, j = (int)(tid - listed - n);
                     listed += n;
+                }
+                if (probe && listed > kList) {   // many alike
+                    probe = false, round = -1, before = 0;
+                    continue;
                 }
                 if (few && listed > kList) {   // (a bound missed by a rounding)
                     few = false;
