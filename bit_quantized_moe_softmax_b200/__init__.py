@@ -12,6 +12,7 @@ buffers with torch, binds them and loads a layer.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -308,6 +309,29 @@ _ACT = {torch.float32: DS4MOE_ACT_F32, torch.bfloat16: DS4MOE_ACT_BF16}
 _Q8 = {torch.float8_e4m3fn: DS4MOE_Q8_E4M3, torch.int8: DS4MOE_Q8_INT8}
 
 
+class _NoFast:
+    """In place of _fastcall.so where it was not built: every call goes the long way."""
+    add_rmsnorm = widen_rows = project = sample = staticmethod(lambda *args: False)
+
+
+_fast = None
+
+
+def _load_fast():
+    """_fastcall.so: checks and call in one step for tensors of the current device on its current stream; False (and
+    nothing launched) where a call is not plainly in order."""
+    global _fast
+    path = os.path.join(_PKG, "_fastcall.so")
+    if os.path.exists(path):
+        lib()  # the library that it calls
+        spec = importlib.util.spec_from_file_location("_fastcall", path)
+        _fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_fast)
+    else:
+        _fast = _NoFast
+    return _fast
+
+
 def _refuse(where: str, msg: str):
     raise Ds4MoeError(-1, where, msg)
 
@@ -368,6 +392,8 @@ def ds4moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residu
     x [n, H] and residual binary32 or bf16; ``sum`` of residual's type (it may be residual itself), ``out`` binary32
     or bf16.  Outputs that are None are not written; at least one is needed.
     """
+    if stream is None and (_fast or _load_fast()).add_rmsnorm(x, weight, eps, residual, sum, out, q, scale, group):
+        return
     where = "ds4moe_add_rmsnorm"
     if x.dim() != 2:
         _refuse(where, "x: %d dimensions, expected [n, hidden]" % x.dim())
@@ -386,6 +412,8 @@ def ds4moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residu
 
 def ds4moe_widen_rows(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, group: int = 128, stream=None):
     """out = q * scale: 8-bit rows of ds4moe_add_rmsnorm (codes [n, H], scales [n, groups]) as binary32 or bf16."""
+    if stream is None and (_fast or _load_fast()).widen_rows(q, scale, out, group):
+        return
     where = "ds4moe_widen_rows"
     if q.dim() != 2:
         _refuse(where, "q: %d dimensions, expected [n, hidden]" % q.dim())
@@ -411,6 +439,8 @@ def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch
     adapter_scale [adapters]; int32 ids [n], -1 for none.  ``work``: uint8 scratch of ds4moe_project_work_bytes
     (allocated here by default).
     """
+    if stream is None and work is None and (_fast or _load_fast()).project(x, W, out, A, B, adapter_scale, ids):
+        return
     where = "ds4moe_project"
     if x.dim() != 2 or W.dim() != 2:
         _refuse(where, "x: expected [n, in], W: [out, in]")
@@ -462,6 +492,8 @@ def ds4moe_sample(logits: torch.Tensor, u: torch.Tensor, token: torch.Tensor, te
 
     token [n] int32; prob [n]: the token's probability; probs [n, vocab]: the filtered distribution.
     """
+    if stream is None and (_fast or _load_fast()).sample(logits, u, token, temperature, top_k, top_p, min_p, prob, probs):
+        return
     where = "ds4moe_sample"
     if logits.dim() != 2:
         _refuse(where, "logits: %d dimensions, expected [n, vocab]" % logits.dim())

@@ -1,14 +1,18 @@
-"""Build libds4moe.so (the C ABI of include/ds4moe.h) for sm_100a with nvcc, in-tree."""
+"""Build libds4moe.so (the C ABI of include/ds4moe.h) for sm_100a with nvcc, in-tree, and _fastcall.so, the Python
+binding's short way to some of its calls (csrc/fastcall.cpp), against torch's headers."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libds4moe.so")
+FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
+FAST = os.path.join(PKG, "_fastcall.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared"]
 
@@ -29,7 +33,41 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def build_fast(force: bool = False) -> str | None:
+    """_fastcall.so; None (and no such file) where it cannot be built: the binding then checks in Python."""
+    header = os.path.join(ROOT, "include", "ds4moe.h")
+    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= max(map(os.path.getmtime, (FAST_SRC, header, __file__))):
+        return FAST
+    tmp = FAST + ".tmp%d" % os.getpid()
+    try:
+        import torch
+        from torch.utils import cpp_extension
+
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(subprocess.check_output(
+            ["which", os.environ.get("NVCC", "nvcc")], text=True).strip())))
+        includes = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+        libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+        subprocess.check_call(["g++", "-O2", "-std=c++20", "-fPIC", "-shared",
+                               "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
+                               *["-I" + i for i in includes], FAST_SRC, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch",
+                               "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libds4moe.so", "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, FAST)
+    except (OSError, ImportError, subprocess.CalledProcessError) as e:
+        print("_fastcall.so was not built: %s" % e)
+        for p in (tmp, FAST):
+            if os.path.exists(p):
+                os.remove(p)
+        return None
+    return FAST
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
+    _build_lib(force, verbose, extra)
+    build_fast(force)
+    return LIB
+
+
+def _build_lib(force: bool, verbose: bool, extra: list[str] | None) -> str:
     if not force and not stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
