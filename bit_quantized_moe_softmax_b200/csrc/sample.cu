@@ -12,13 +12,18 @@
 // the split of a row over CTAs cannot change a result.  exp is taken in
 // binary64, since a draw near a border is decided by the weights' last bits.
 //
-// A row belongs to a cluster of up to eight CTAs that keep it in shared memory
+// A row belongs to a cluster of up to sixteen CTAs that keep it in shared memory
 // as binary32 (up to 32,768 tokens each): one read of the logits from HBM,
 // every further pass is on chip, and sums meet through distributed shared
 // memory.  A filter's threshold is found by histograms of 2,048 bins: first
-// over M - l in small steps; the tokens of the bin that holds the prefix's end
-// are then sorted, or, where there are more than 512 (logits of few bits have
-// many ties), counted over their keys' bits.
+// over M - l in small steps (for a small top-k, of each thread's largest logit
+// alone); the tokens of the bin that holds the prefix's end are then sorted, or,
+// where there are more than 512 (logits of few bits have many ties), counted
+// over their keys' bits.  Where all tokens down to that bin are at most 512,
+// they are sorted together and the remaining filters and the draw need no
+// other.  131,072 binary32 logits: one row 9 us without filters, 16 with all;
+// 256 rows 104 us without, 290 with top-p (7 % of HBM's rate: what bounds them
+// is the issue of some 70 to 160 instructions per 32 tokens).
 #include <cooperative_groups.h>
 
 #include "ds4moe_internal.cuh"
