@@ -314,15 +314,16 @@ static cudaError_t shrink_launch(const ShrinkArgs& s, dim3 grid, cudaStream_t st
     return cudaLaunchKernelEx(&cfg, k_adapter_shrink<NT, kShRows>, s);
 }
 
-// 8 to 64 rows (a decode batch; fewer are faster by the MMAs: 14 against 20 us for
-// one row at 4096 x 4096): a block of the K axis per adapter would be
-// zero but for a row or two, so the warps that drain the accumulators add the
-// adapters themselves, in binary32, while the MMAs run: a lane has one output
-// feature and reads its `rank` values of B for each row (a warp: consecutive
-// memory), eight rows' loads in flight.  acc[i] += B[id][o] . t for rows
-// lo + i < hi; ts, ids: t [rows][rank] and the rows' adapters (or -1) in shared
-// memory.
-__device__ __forceinline__ void adapter_rows(const ProjectArgs& a, const float* ts, const int* ids, int o, int lo, int hi,
+// 8 to 64 rows (a decode batch; fewer are faster by the MMAs, 14 against 20 us for
+// one row at 4096 x 4096, and so are more, 37 against 41 us for 128 rows of 64
+// adapters): a block of the K axis per adapter would be zero but for a row or
+// two, so the warps that drain the accumulators add the adapters themselves, in
+// binary32, while the MMAs run: a lane has one output feature and reads its
+// `rank` values of B for each row (a warp: consecutive memory), eight rows' loads
+// in flight.  Of a split tile each CTA adds and stages the rows that it finishes.
+// acc[i] += B[id][o] . t for the first `rows` of the CTA's rows; ts, ids: their t
+// [rows][rank] and adapters (or -1) in shared memory.
+__device__ __forceinline__ void adapter_rows(const ProjectArgs& a, const float* ts, const int* ids, int o, int rows,
                                              float (&acc)[kRowsMax]) {
 #pragma unroll
     for (int i = 0; i < kRowsMax; ++i) acc[i] = 0.f;
@@ -330,18 +331,18 @@ __device__ __forceinline__ void adapter_rows(const ProjectArgs& a, const float* 
     const size_t stride = (size_t)a.fout * a.rank;
 #pragma unroll
     for (int c = 0; c < kRowsMax; c += 8) {
-        if (lo + c >= hi) break;
+        if (c >= rows) break;
         for (int k = 0; k < a.rank; k += 8) {
             uint4 w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int id = lo + c + j < hi ? ids[lo + c + j] : -1;
+                const int id = c + j < rows ? ids[c + j] : -1;
                 w[j] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(B + (size_t)id * stride + k)) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int row = lo + c + j;
-                if (row < hi && ids[row] >= 0) {
+                const int row = c + j;
+                if (row < rows && ids[row] >= 0) {
                     const float4 t0 = *reinterpret_cast<const float4*>(ts + row * a.rank + k);
                     const float4 t1 = *reinterpret_cast<const float4*>(ts + row * a.rank + k + 4);
                     const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
@@ -357,14 +358,14 @@ __device__ __forceinline__ void adapter_rows(const ProjectArgs& a, const float* 
     }
 }
 
-// t and the adapters of up to 64 rows into shared memory, by `threads` threads
-// that meet at barrier 1.
-__device__ __forceinline__ void stage_rows(const ProjectArgs& a, float* ts, int* ids, int i0, int threads) {
+// t and the adapters of rows lo .. lo + rows - 1 into shared memory, by
+// `threads` threads that meet at barrier 1.
+__device__ __forceinline__ void stage_rows(const ProjectArgs& a, float* ts, int* ids, int lo, int rows, int i0, int threads) {
     griddep_wait();   // t is the first kernel's
-    for (int i = i0; i < a.n * a.rank / 4; i += threads)
-        reinterpret_cast<float4*>(ts)[i] = __ldcg(reinterpret_cast<const float4*>(a.rows) + i);
-    for (int i = i0; i < a.n; i += threads) {
-        const int id = __ldg(a.ids + i);
+    const float4* src = reinterpret_cast<const float4*>(a.rows + (size_t)lo * a.rank);
+    for (int i = i0; i < rows * a.rank / 4; i += threads) reinterpret_cast<float4*>(ts)[i] = __ldcg(src + i);
+    for (int i = i0; i < rows; i += threads) {
+        const int id = __ldg(a.ids + lo + i);
         ids[i] = (unsigned)id < (unsigned)a.n_adapters ? id : -1;
     }
     named_sync(1, threads);
@@ -631,16 +632,16 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
         const int qd = warp & 3;   // TMEM lanes 32 qd .. 32 qd + 31
         uint32_t use = 0;
         float* ts = reinterpret_cast<float*>(st + a.stages * stage_bytes);
-        if constexpr (Rows) stage_rows(a, ts, S.ids, tid - 128, 128);
-        const int per = (a.bn + a.split - 1) / a.split;   // rows that this CTA of a split tile finishes
+        const int per = (a.bn + a.split - 1) / a.split, lo = per * rank_in;   // rows that this CTA of a split tile finishes
+        const int mine = max(0, min(a.n, lo + per) - lo);                      // (Rows: there is one tile along the rows)
+        if constexpr (Rows) stage_rows(a, ts, S.ids, lo, mine, tid - 128, 128);
         for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
             const int buf = use & 1;
             const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + buf * a.bn;
             const int o = tile / a.row_tiles * kPM + 32 * qd + lane, r0 = tile % a.row_tiles * a.bn;
             const int rows = min(a.bn, a.n - r0);
             float acc[Rows ? kRowsMax : 1];
-            const int lo = per * rank_in;
-            if constexpr (Rows) adapter_rows(a, ts, S.ids, o, lo, min(rows, lo + per), acc);
+            if constexpr (Rows) adapter_rows(a, ts, S.ids, o, mine, acc);
             if (!mbar_wait(&S.accF[buf], (use >> 1) & 1, err)) S.abort = 1;
             const bool ok = !S.abort;   // a wait that ran out leaves NaN in the tile
             tc_fence_after();
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
                 if constexpr (Rows) {
 #pragma unroll
                     for (int j = 0; j < kRowsMax / 2; ++j)
-                        if (j < per && lo + j < rows) part[(lo + j) * kPM] += acc[j];
+                        if (j < mine) part[(lo + j) * kPM] += acc[j];
                 }
             } else {
                 store_tile<Rows>(a, taddr, o, lane, r0, rows, ok, acc);
@@ -894,12 +895,12 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
         const int qd = warp & 3, m = (warp - 4) >> 2;   // TMEM lanes 32 qd .., accumulator m
         uint32_t use = 0;
         float* ts = reinterpret_cast<float*>(st + a.stages * stage_bytes);
-        if constexpr (Rows) stage_rows(a, ts, S.ids, tid - 128, kPairThreads - 128);
+        if constexpr (Rows) stage_rows(a, ts, S.ids, 0, a.n, tid - 128, kPairThreads - 128);
         for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
             const int o = tile / a.row_tiles * (4 * kPM) + m * (2 * kPM) + r * kPM + 32 * qd + lane, r0 = tile % a.row_tiles * a.bn;
             const int rows = min(a.bn, a.n - r0);
             float acc[Rows ? kRowsMax : 1];
-            if constexpr (Rows) adapter_rows(a, ts, S.ids, o, 0, rows, acc);
+            if constexpr (Rows) adapter_rows(a, ts, S.ids, o, rows, acc);
             if (!mbar_wait(&S.accF, use & 1, err)) stop();
             const bool ok = !S.abort;
             tc_fence_after();
@@ -1035,7 +1036,7 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     const int stage = wk.pair ? 2 * kPStageA + p.bn / 2 * kPK * 2 : kPStageA + p.bn * kPK * 2;
     // with adapters, room for a CTA of the first kernel beside this one, so that W streams meanwhile (one row at
     // 4096 x 4096: 14 us, without it 19)
-    const int t_bytes = p.rows ? p.n * p.rank * 4 : 0;
+    const int t_bytes = p.rows ? (p.bn + p.split - 1) / p.split * p.rank * 4 : 0;
     const int room = p.rows || (p.counts && p.bn <= kRowsMax) ? kPSmemRows : p.counts && p.rank <= 64 ? kPSmemEntries : kPSmem;
     p.stages = (room - t_bytes) / stage < kPMaxStages ? (room - t_bytes) / stage : kPMaxStages;
     const int smem = 1024 + p.stages * stage + t_bytes;   // the partial sums of a split tile (512 bytes per row) fit as well
