@@ -21,7 +21,7 @@
 // where there are more than 512 (logits of few bits have many ties), counted
 // over their keys' bits.  Where all tokens down to that bin are at most 512,
 // they are sorted together and the remaining filters and the draw need no
-// other.  131,072 binary32 logits: one row 9 us without filters, 16 with all;
+// other.  131,072 binary32 logits: one row 9 us without filters, 15 with all;
 // 256 rows 104 us without, 290 with top-p (7 % of HBM's rate: what bounds them
 // is the issue of some 70 to 160 instructions per 32 tokens).
 #include <cooperative_groups.h>
@@ -255,8 +255,8 @@ __device__ __noinline__ u64 sort_desc(SampleSmem& S, u64 v) {
 
 }  // namespace
 
-template <bool BF, int C>
 // (sixteen CTAs, for a few rows: all registers, 16.0 -> 14.7 us; else two CTAs per SM, 290 against 390 us for 256 rows)
+template <bool BF, int C>
 __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
     extern __shared__ __align__(16) float vals[];   // [kSW][a.seg]: each warp's share of the CTA's tokens, in index order
     __shared__ SampleSmem S;
