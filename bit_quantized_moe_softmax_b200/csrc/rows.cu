@@ -324,11 +324,14 @@ __device__ __forceinline__ void widen4(uint32_t w, int fmt, float (&v)[4]) {
 // row width costs as much as the rest otherwise).  A thread's pieces are in
 // flight together: two where there are enough threads all the same (11,709 x
 // 4096 to bf16: 24.0 us, one 32.5 us), one for few rows (61 x 2050 to binary32:
-// 2.9 us, two 3.8 us).
+// 2.9 us, two 3.8 us).  Sixteen bf16 values are one 32-byte store, which needs a
+// 32-byte address; out is 16-byte aligned (a view of rows may begin between),
+// and then they are two stores.
 template <bool OBF, typename I, int kWidenPieces>
 __global__ void __launch_bounds__(256) k_widen_rows(const uint8_t* q, int fmt, const float* scale, int shift, int H,
                                                     I total, void* out) {
     const int ngroups = shift ? (H + (1 << shift) - 1) >> shift : 1;
+    const bool out32 = ((uintptr_t)out & 31) == 0;   // the same for every piece of 32 bytes
     uint4 raw[kWidenPieces];
     float first[kWidenPieces];
     I row[kWidenPieces];
@@ -391,9 +394,16 @@ __global__ void __launch_bounds__(256) k_widen_rows(const uint8_t* q, int fmt, c
         }
         if (cnt == 16) {
             if constexpr (OBF) {
-                st_global_v8(static_cast<uint16_t*>(out) + i0, bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
-                             bf16x2(v[6], v[7]), bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]),
-                             bf16x2(v[14], v[15]));
+                uint32_t b[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) b[j] = bf16x2(v[2 * j], v[2 * j + 1]);
+                uint16_t* o = static_cast<uint16_t*>(out) + i0;
+                if (out32) {
+                    st_global_v8(o, b[0], b[1], b[2], b[3], b[4], b[5], b[6], b[7]);
+                } else {
+                    reinterpret_cast<uint4*>(o)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+                    reinterpret_cast<uint4*>(o)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+                }
             } else {
                 float* o = static_cast<float*>(out) + i0;
 #pragma unroll
