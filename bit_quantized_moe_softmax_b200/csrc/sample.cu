@@ -158,6 +158,11 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {   // inclusive
     return v;
 }
 
+// The first meeting of a cluster's CTAs in two halves: shared memory of a peer may
+// be written only once the peer runs, and between the halves the row is read.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Sums of 64 bins of this CTA's histogram `buf` to every CTA of the cluster.
 // The histogram must be complete; a cluster barrier follows before find_bin.
 template <int C>
@@ -260,6 +265,7 @@ template <bool BF, int C>
 __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
     extern __shared__ __align__(16) float vals[];   // [kSW][a.seg]: each warp's share of the CTA's tokens, in index order
     __shared__ SampleSmem S;
+    if (C > 1) cluster_arrive();
     cg::cluster_group cl = cg::this_cluster();
     const int r = C == 1 ? 0 : (int)cl.block_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / C;
@@ -334,6 +340,7 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
 #pragma unroll
     for (int w = 0; w < kSW; ++w) mx = fmaxf(mx, S.wmax[w]);
     if (C > 1) {
+        cluster_wait();
         if (tid < C) cl.map_shared_rank(S.mx, tid)[r] = mx;
         cl.sync();
 #pragma unroll
