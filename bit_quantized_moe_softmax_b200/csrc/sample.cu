@@ -84,7 +84,7 @@ __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(
 // tested for, and the unit's sums keep the offset of the conversion.
 struct Weigh {
     double M, c;           // c = 128 log2(e) / T, at most where one step below M already weighs nothing
-    float Mf, cf;
+    float half, c2;        // M / 2 and 2 c: no difference of two finite halves overflows
     double reach;          // 8192 / c
     float low;             // M - reach
     bool flat;             // T so large that low is the lowest binary32 value: -infinity is tested for
@@ -96,24 +96,21 @@ struct Weigh {
         reach = fmax(8192.0 / (kTab * 1.44269504088896340736) * (double)T, 8192e-38);   // 8192 / c
         tab = table;
     }
-    // the maximum; everything scaled by 2^-shift
-    __device__ __forceinline__ void set_maximum(float m, int shift) {
-        const double by = __hiloint2double((1023 + shift) << 20, 0);
-        c = fmin(c * by, 1e38), reach /= by;
+    __device__ __forceinline__ void set_maximum(float m) {
         const float below = __uint_as_float(m > 0.f ? __float_as_uint(m) - 1 : m < 0.f ? __float_as_uint(m) + 1 : 0x80000001u);
         // a power of two (2^104 at the lowest value), and 1 / step by its exponent
         const double step = below == kNegInf ? 0x1p104 : (double)m - (double)below;
         const double most = 6000.0 * __hiloint2double(0x7fe00000 - __double2hiint(step), 0);
         if (c > most) c = most, reach = 8192.0 / 6000.0 * step;
-        M = m, Mf = m;
-        cf = (float)c;
+        M = m, half = 0.5f * m;
+        c2 = (float)(2.0 * c);
         const double l = (double)m - reach;
         flat = !(l > -3.4e38);
         low = flat ? -3.402823466e38f : __double2float_rd(l);
     }
     __device__ __forceinline__ double operator()(float l) const {
         l = fmaxf(l, low);
-        const int n = __float_as_int(fmaf(l - Mf, cf, 12582912.f));        // 0x4b400000 + the nearest integer of y
+        const int n = __float_as_int(fmaf(fmaf(l, 0.5f, -half), c2, 12582912.f));        // 0x4b400000 + the nearest integer of y
         const double k = __hiloint2double(0x43300000, n) - (4503599627370496.0 + 1262485504.0);
         const double r = fma((double)l - M, c, -k);
         constexpr double h = 0.69314718055994530942 / kTab;
@@ -136,7 +133,8 @@ struct Weigh {
 };
 
 // Bin of the first histogram: (M - l) in steps, the last bin for all beyond.
-// Monotone in l, so any rounding is as good.
+// Monotone in l, so any rounding is as good, and a difference that overflows
+// falls into the last bin like all far ones.
 struct Coarse {
     float M, step;   // 1 / step length, between 1e-38 and 1e38: no product of 0 and infinity
     __device__ __forceinline__ uint32_t operator()(float l) const {
@@ -281,7 +279,6 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
     const double inv = 1.0 / (double)T;
     Weigh weigh;
     weigh.set_temperature(T, S.tab);
-    int shift = 0;
 
     // ---- the row into shared memory, and its maximum; a NaN counts as -infinity
     float mx = kNegInf;
@@ -363,16 +360,10 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
         mx = 0.f;
         own_max = own_max == INFINITY ? 0.f : kNegInf;
         __syncthreads();
-    } else if (mx > 1e37f) {   // no difference of logits may overflow: everything by 2^-8
-        for (int i = tid; i < kSW * a.seg; i += kST) vals[i] *= 0.00390625f;
-        mx *= 0.00390625f;
-        own_max *= 0.00390625f;
-        shift = 8;
-        __syncthreads();
     }
     const bool by_k = K >= 1 && K < a.V, by_p = P < 1.f, by_m = mp > 0.f;
     const double minw = fmin((double)mp, 1.0);
-    weigh.set_maximum(mx, shift);
+    weigh.set_maximum(mx);
     const int s0 = warp * a.seg;   // this warp's tokens: s0 .. s0 + seg - 1
 
     // ---- the prefix that top-k and top-p keep: tokens above thr, and those at it up to index last of the row
@@ -441,7 +432,7 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
         if (!(mass ? by_p : by_k) || small) continue;
         // steps of 1/128 of a temperature for masses, of 1/64 for counts: a few hundred tokens at most in the
         // bins that matter
-        const Coarse coarse{mx, (float)fmin(fmax(mass ? inv * (shift ? 32768.0 : 128.0) : 64.0, 1e-38), 1e38)};
+        const Coarse coarse{mx, (float)fmin(fmax(mass ? inv * 128.0 : 64.0, 1e-38), 1e38)};
         u64 target = (u64)K, before = 0, own = 0;
         uint32_t bin = 0, lo = 0, hi = 0;
         bool found = false, few = false;

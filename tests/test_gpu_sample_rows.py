@@ -1,9 +1,11 @@
 """ds4moe_sample on many rows at once, where the CTAs of a row start apart from each
-other, against torch on the device."""
+other, against torch on the device; and on logits far apart, against the 64-bit
+reference."""
 import pytest
 import torch
 
 import bit_quantized_moe_softmax_b200 as m
+from tests.test_gpu_sample import _check
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +35,28 @@ def test_maximum_in_any_share(V, n):
             token.fill_(-7)
             m.ds4moe_sample(l, u, token, temperature=temperature, top_p=None if temperature is zero else zero + 0.5, prob=prob)
             assert torch.equal(token.long(), at) and bool((prob == 1).all())
+
+
+@pytest.mark.parametrize("T", [1.0, 1e30, 1e36, 1e37, 3e38, float("inf")])
+@pytest.mark.parametrize("V", [40, 9000])
+def test_largest_logit_beside_the_lowest(V, T):
+    """Row maxima from 1e29 to binary32's largest beside tokens at its lowest value, whose difference binary32 cannot
+    hold, at temperatures that give them weight all the same."""
+    tops = [1e29, 1e31, 1e32, 5e36, 1e37, 1.1e37, 1e38, 3.4e38, -1e32, 5.0]
+    l = torch.randn(len(tops), V, generator=torch.Generator().manual_seed(V))
+    l[:, 2::3] = torch.finfo(torch.float32).min
+    for i, top in enumerate(tops):
+        l[i, 1::3] = top * (1 - 0.5 * torch.rand(l[i, 1::3].shape, generator=torch.Generator().manual_seed(i)))
+        l[i, 7] = top if top > 0 else 6.0
+    u = torch.linspace(0.03, 0.98, len(tops))
+    for f in (dict(), dict(k=V // 2), dict(p=0.6), dict(k=V - 3, p=0.9, mp=0.01)):
+        _check(l, u, T=T, **f)
+
+
+def test_order_of_tiny_logits_beside_a_huge_one():
+    """Neighbours in binary32 keep their order, however large the row's maximum."""
+    V = 600
+    l = (torch.arange(V, dtype=torch.int32) + 1).view(torch.float32).repeat(3, 1)   # the smallest subnormals, ascending
+    l[:, 0] = torch.tensor([2e37, 3e38, 1.0])
+    for k in (3, 40):
+        _check(l, torch.tensor([0.999, 0.999, 0.5]), T=float("inf"), k=k)
