@@ -72,6 +72,17 @@ __device__ __forceinline__ uint32_t code8x2(float a, float b, int fmt) {
 
 }  // namespace
 
+// A launch with its own status: what an earlier call of the thread left behind is
+// not this launch's (a caller told of a failure would make the call again).
+template <typename... P, typename... A>
+static cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, kernel, (P)args...);
+}
+
 // ---------------------------------------------------------------- residual addition and norm
 // s = x + r (one binary32 add, rounded to r's type where that is stored);
 // y = (s * rstd) * w with rstd = 1 / sqrt(mean(s^2) + eps); optionally y as
@@ -263,16 +274,15 @@ __global__ void __launch_bounds__(CH == 4 ? 512 : 1024) k_add_rmsnorm(AddNormArg
 }
 
 template <bool XBF, int RT, bool VEC>
-static void norm_launch(const AddNormArgs& a, int ch, dim3 grid, dim3 block, cudaStream_t st) {
-    if (ch == 1) k_add_rmsnorm<XBF, RT, 1, VEC><<<grid, block, 0, st>>>(a);
-    else if (ch == 2) k_add_rmsnorm<XBF, RT, 2, VEC><<<grid, block, 0, st>>>(a);
-    else k_add_rmsnorm<XBF, RT, 4, VEC><<<grid, block, 0, st>>>(a);
+static cudaError_t norm_launch(const AddNormArgs& a, int ch, dim3 grid, dim3 block, cudaStream_t st) {
+    if (ch == 1) return launch(k_add_rmsnorm<XBF, RT, 1, VEC>, grid, block, st, a);
+    if (ch == 2) return launch(k_add_rmsnorm<XBF, RT, 2, VEC>, grid, block, st, a);
+    return launch(k_add_rmsnorm<XBF, RT, 4, VEC>, grid, block, st, a);
 }
 
 template <bool XBF, int RT>
-static void norm_launch_v(const AddNormArgs& a, bool vec, int ch, dim3 grid, dim3 block, cudaStream_t st) {
-    if (vec) norm_launch<XBF, RT, true>(a, ch, grid, block, st);
-    else norm_launch<XBF, RT, false>(a, ch, grid, block, st);
+static cudaError_t norm_launch_v(const AddNormArgs& a, bool vec, int ch, dim3 grid, dim3 block, cudaStream_t st) {
+    return vec ? norm_launch<XBF, RT, true>(a, ch, grid, block, st) : norm_launch<XBF, RT, false>(a, ch, grid, block, st);
 }
 
 cudaError_t launch_add_rmsnorm(AddNormArgs a, bool x_bf16, int res_kind, bool vec, int n_sm, cudaStream_t st) {
@@ -290,15 +300,13 @@ cudaError_t launch_add_rmsnorm(AddNormArgs a, bool x_bf16, int res_kind, bool ve
     const dim3 block(32 * (solo ? rows_per_cta : a.warps_per_row));
     const dim3 grid((unsigned)((a.n + rows_per_cta - 1) / rows_per_cta));
     if (x_bf16) {
-        if (res_kind == 0) norm_launch_v<true, 0>(a, vec, ch, grid, block, st);
-        else if (res_kind == 1) norm_launch_v<true, 1>(a, vec, ch, grid, block, st);
-        else norm_launch_v<true, 2>(a, vec, ch, grid, block, st);
-    } else {
-        if (res_kind == 0) norm_launch_v<false, 0>(a, vec, ch, grid, block, st);
-        else if (res_kind == 1) norm_launch_v<false, 1>(a, vec, ch, grid, block, st);
-        else norm_launch_v<false, 2>(a, vec, ch, grid, block, st);
+        if (res_kind == 0) return norm_launch_v<true, 0>(a, vec, ch, grid, block, st);
+        if (res_kind == 1) return norm_launch_v<true, 1>(a, vec, ch, grid, block, st);
+        return norm_launch_v<true, 2>(a, vec, ch, grid, block, st);
     }
-    return cudaGetLastError();
+    if (res_kind == 0) return norm_launch_v<false, 0>(a, vec, ch, grid, block, st);
+    if (res_kind == 1) return norm_launch_v<false, 1>(a, vec, ch, grid, block, st);
+    return norm_launch_v<false, 2>(a, vec, ch, grid, block, st);
 }
 
 // ---------------------------------------------------------------- widening of 8-bit rows
@@ -419,13 +427,13 @@ __global__ void __launch_bounds__(256) k_widen_rows(const uint8_t* q, int fmt, c
 }
 
 template <bool OBF, int P>
-static void widen_launch(const uint8_t* q, int fmt, const float* scale, int shift, int H, int64_t total, void* out,
-                         cudaStream_t st) {
+static cudaError_t widen_launch(const uint8_t* q, int fmt, const float* scale, int shift, int H, int64_t total, void* out,
+                                cudaStream_t st) {
     const int64_t per = 256 * P * 16, ctas = (total + per - 1) / per;
+    const dim3 grid((unsigned)ctas), block(256);
     if (ctas * per < ((int64_t)1 << 32))
-        k_widen_rows<OBF, uint32_t, P><<<(unsigned)ctas, 256, 0, st>>>(q, fmt, scale, shift, H, (uint32_t)total, out);
-    else
-        k_widen_rows<OBF, uint64_t, P><<<(unsigned)ctas, 256, 0, st>>>(q, fmt, scale, shift, H, (uint64_t)total, out);
+        return launch(k_widen_rows<OBF, uint32_t, P>, grid, block, st, q, fmt, scale, shift, H, total, out);
+    return launch(k_widen_rows<OBF, uint64_t, P>, grid, block, st, q, fmt, scale, shift, H, total, out);
 }
 
 cudaError_t launch_widen_rows(const uint8_t* q, int fmt, const float* scale, int group, int n, int H, void* out,
@@ -433,14 +441,11 @@ cudaError_t launch_widen_rows(const uint8_t* q, int fmt, const float* scale, int
     const int shift = group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : 0;
     const int64_t total = (int64_t)n * H;
     const bool few = total < ((int64_t)1 << 22);   // 1,024 CTAs of one piece per thread
-    if (out_bf16) {
-        if (few) widen_launch<true, 1>(q, fmt, scale, shift, H, total, out, st);
-        else widen_launch<true, 2>(q, fmt, scale, shift, H, total, out, st);
-    } else {
-        if (few) widen_launch<false, 1>(q, fmt, scale, shift, H, total, out, st);
-        else widen_launch<false, 2>(q, fmt, scale, shift, H, total, out, st);
-    }
-    return cudaGetLastError();
+    if (out_bf16)
+        return few ? widen_launch<true, 1>(q, fmt, scale, shift, H, total, out, st)
+                   : widen_launch<true, 2>(q, fmt, scale, shift, H, total, out, st);
+    return few ? widen_launch<false, 1>(q, fmt, scale, shift, H, total, out, st)
+               : widen_launch<false, 2>(q, fmt, scale, shift, H, total, out, st);
 }
 
 }  // namespace ds4
