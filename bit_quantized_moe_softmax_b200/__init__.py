@@ -318,8 +318,9 @@ _fast = None
 
 
 def _load_fast():
-    """_fastcall.so: checks and call in one step for tensors of the current device on its current stream; False (and
-    nothing launched) where a call is not plainly in order."""
+    """_fastcall.so: checks and call in one step for tensors of the current device on its current stream: True, or
+    False (and nothing launched) where a call is not plainly in order, or the status of one that failed behind its
+    checks and so is not made again."""
     global _fast
     path = os.path.join(_PKG, "_fastcall.so")
     if os.path.exists(path):
@@ -392,9 +393,11 @@ def ds4moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residu
     x [n, H] and residual binary32 or bf16; ``sum`` of residual's type (it may be residual itself), ``out`` binary32
     or bf16.  Outputs that are None are not written; at least one is needed.
     """
-    if stream is None and (_fast or _load_fast()).add_rmsnorm(x, weight, eps, residual, sum, out, q, scale, group):
-        return
     where = "ds4moe_add_rmsnorm"
+    if stream is None:
+        done = (_fast or _load_fast()).add_rmsnorm(x, weight, eps, residual, sum, out, q, scale, group)
+        if done:
+            return None if done is True else _ok(done, where)
     if x.dim() != 2:
         _refuse(where, "x: %d dimensions, expected [n, hidden]" % x.dim())
     n, H = x.shape
@@ -412,9 +415,11 @@ def ds4moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residu
 
 def ds4moe_widen_rows(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, group: int = 128, stream=None):
     """out = q * scale: 8-bit rows of ds4moe_add_rmsnorm (codes [n, H], scales [n, groups]) as binary32 or bf16."""
-    if stream is None and (_fast or _load_fast()).widen_rows(q, scale, out, group):
-        return
     where = "ds4moe_widen_rows"
+    if stream is None:
+        done = (_fast or _load_fast()).widen_rows(q, scale, out, group)
+        if done:
+            return None if done is True else _ok(done, where)
     if q.dim() != 2:
         _refuse(where, "q: %d dimensions, expected [n, hidden]" % q.dim())
     n, H = q.shape
@@ -439,9 +444,11 @@ def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch
     adapter_scale [adapters]; int32 ids [n], -1 for none.  ``work``: uint8 scratch of ds4moe_project_work_bytes
     (allocated here by default).
     """
-    if stream is None and work is None and (_fast or _load_fast()).project(x, W, out, A, B, adapter_scale, ids):
-        return
     where = "ds4moe_project"
+    if stream is None and work is None:
+        done = (_fast or _load_fast()).project(x, W, out, A, B, adapter_scale, ids)
+        if done:
+            return None if done is True else _ok(done, where)
     if x.dim() != 2 or W.dim() != 2:
         _refuse(where, "x: expected [n, in], W: [out, in]")
     n, fin = x.shape
@@ -492,9 +499,11 @@ def ds4moe_sample(logits: torch.Tensor, u: torch.Tensor, token: torch.Tensor, te
 
     token [n] int32; prob [n]: the token's probability; probs [n, vocab]: the filtered distribution.
     """
-    if stream is None and (_fast or _load_fast()).sample(logits, u, token, temperature, top_k, top_p, min_p, prob, probs):
-        return
     where = "ds4moe_sample"
+    if stream is None:
+        done = (_fast or _load_fast()).sample(logits, u, token, temperature, top_k, top_p, min_p, prob, probs)
+        if done:
+            return None if done is True else _ok(done, where)
     if logits.dim() != 2:
         _refuse(where, "logits: %d dimensions, expected [n, vocab]" % logits.dim())
     n, V = logits.shape

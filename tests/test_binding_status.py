@@ -1,0 +1,54 @@
+"""The binding of the operators around the layer, without a GPU: what becomes of the
+short way's answer."""
+import types
+
+import pytest
+import torch
+
+import bit_quantized_moe_softmax_b200 as m
+
+
+def _calls():
+    x = torch.zeros(2, 8)
+    bf, i = x.bfloat16(), torch.zeros(2, dtype=torch.int32)
+    return [("add_rmsnorm", lambda: m.ds4moe_add_rmsnorm(x, x[0], 1e-6, out=x.clone())),
+            ("widen_rows", lambda: m.ds4moe_widen_rows(x.to(torch.int8), x[:, :1].contiguous(), x.clone())),
+            ("project", lambda: m.ds4moe_project(bf, bf.clone(), bf.clone())),
+            ("sample", lambda: m.ds4moe_sample(x, x[:, 0].contiguous(), i))]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from bit_quantized_moe_softmax_b200 import build
+
+    build.build()
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_a_failure_behind_the_checks_is_raised_and_the_call_not_repeated(monkeypatch, which):
+    """The norm adds into its residual in place: a second launch would add twice."""
+    name, call = _calls()[which]
+    seen = []
+
+    def fails(*args):
+        seen.append(name)
+        return -5   # DS4MOE_ERR_CUDA
+
+    monkeypatch.setattr(m, "_fast", types.SimpleNamespace(**{name: fails}))
+    monkeypatch.setattr(m, "_call", lambda *args: seen.append("again"))
+    monkeypatch.setattr(m, "_tensors", lambda *args: None)
+    with pytest.raises(m.Ds4MoeError) as e:
+        call()
+    assert e.value.status == -5 and seen == [name]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_done_and_not_in_order(monkeypatch, which):
+    name, call = _calls()[which]
+    for answer, long_way in ((True, []), (False, ["long"])):
+        seen = []
+        monkeypatch.setattr(m, "_fast", types.SimpleNamespace(**{name: lambda *args: answer}))
+        monkeypatch.setattr(m, "_call", lambda *args: seen.append("long"))
+        monkeypatch.setattr(m, "_tensors", lambda *args: None)
+        call()
+        assert seen == long_way
