@@ -39,7 +39,7 @@ EXPORTS = ("ds4moe_create", "ds4moe_destroy", "ds4moe_weight_bytes", "ds4moe_wor
            "ds4moe_host_sync", "ds4moe_probe", "ds4moe_selftest_wait",
            "ds4moe_permutation", "ds4moe_pack_q4k", "ds4moe_forward_chain", "ds4moe_forward_routed",
            "ds4moe_combine_slots", "ds4moe_add_rmsnorm", "ds4moe_widen_rows", "ds4moe_project",
-           "ds4moe_project_work_bytes", "ds4moe_get_project_error", "ds4moe_sample")
+           "ds4moe_project_work_bytes", "ds4moe_get_project_error", "ds4moe_selftest_project_wait", "ds4moe_sample")
 
 
 class ds4moe_shape(ctypes.Structure):
@@ -103,6 +103,7 @@ def lib() -> ctypes.CDLL:
             "ds4moe_project": ([vp, i32, vp, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp], i32),
             "ds4moe_project_work_bytes": ([i32, i32, i32, i32, i32], sz),
             "ds4moe_get_project_error": ([vp, ctypes.POINTER(i32)], i32),
+            "ds4moe_selftest_project_wait": ([vp, i32, vp, i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, sz, i32, vp], i32),
             "ds4moe_sample": ([vp, i32, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
         }
         for name, (args, res) in sig.items():
@@ -449,6 +450,10 @@ def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch
         done = (_fast or _load_fast()).project(x, W, out, A, B, adapter_scale, ids)
         if done:
             return None if done is True else _ok(done, where)
+    _project(where, lib().ds4moe_project, x, W, out, A, B, adapter_scale, ids, work, stream)
+
+
+def _project(where, fn, x, W, out, A, B, adapter_scale, ids, work, stream, *more):
     if x.dim() != 2 or W.dim() != 2:
         _refuse(where, "x: expected [n, in], W: [out, in]")
     n, fin = x.shape
@@ -478,8 +483,8 @@ def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch
         elif work.get_device() != dev or not work.is_contiguous():
             _refuse(where, "work: contiguous on %s expected" % x.device)
         wb = work.numel() * work.element_size()
-    _call(where, dev, stream, lib().ds4moe_project, x.data_ptr(), n, W.data_ptr(), fin, fout, _ptr(A), _ptr(B),
-          _ptr(adapter_scale), na, rank, _ptr(ids), out.data_ptr(), _ptr(work), wb)
+    _call(where, dev, stream, fn, x.data_ptr(), n, W.data_ptr(), fin, fout, _ptr(A), _ptr(B), _ptr(adapter_scale), na, rank,
+          _ptr(ids), out.data_ptr(), _ptr(work), wb, *more)
 
 
 def ds4moe_get_project_error(stream=None) -> int:
@@ -488,6 +493,12 @@ def ds4moe_get_project_error(stream=None) -> int:
     if st not in (0, -6):
         _ok(st, "ds4moe_get_project_error")
     return code.value
+
+
+def ds4moe_selftest_project_wait(x, W, out, A=None, B=None, adapter_scale=None, ids=None, tiles: int = 0, stream=None):
+    """ds4moe_project whose waits give up at once from each CTA's ``tiles``-th tile on: NaN there, and the error word."""
+    _project("ds4moe_selftest_project_wait", lib().ds4moe_selftest_project_wait, x, W, out, A, B, adapter_scale, ids, None,
+             stream, tiles)
 
 
 def ds4moe_sample(logits: torch.Tensor, u: torch.Tensor, token: torch.Tensor, temperature: torch.Tensor | None = None,

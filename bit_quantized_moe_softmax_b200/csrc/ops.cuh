@@ -73,6 +73,7 @@ struct ProjectArgs {
     const __nv_bfloat16* B;     // [n_adapters][fout][rank]
     const int32_t* ids;         // [n]
     int n_adapters;
+    int in_time;                // tiles of each CTA (or pair) whose waits have their limit; those behind give up at once
     int bn, row_tiles, cap, kblocks, tiles, split, stages;   // set by the launcher
 };
 struct ProjectWork {            // layout of the caller's work buffer

@@ -146,9 +146,9 @@ size_t ds4moe_project_work_bytes(int32_t n, int32_t in_features, int32_t out_fea
     return project_work(n, in_features, out_features, n_adapters, rank).total;
 }
 
-ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_t in_features, int32_t out_features,
+static ds4moe_status project(const void* d_x, int32_t n, const void* d_W, int32_t in_features, int32_t out_features,
                              const void* d_A, const void* d_B, const float* d_scale, int32_t n_adapters, int32_t rank,
-                             const int32_t* d_ids, void* d_out, void* d_work, size_t work_bytes, void* stream) {
+                             const int32_t* d_ids, void* d_out, void* d_work, size_t work_bytes, int in_time, void* stream) {
     const ds4moe_status s = check_project(n, in_features, out_features, n_adapters, rank);
     if (s != DS4MOE_OK) return s;
     if (n == 0) return DS4MOE_OK;
@@ -175,6 +175,7 @@ ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_
     p.n = sh.n = n;
     p.fin = sh.fin = in_features;
     p.fout = out_features;
+    p.in_time = in_time;
     sh.x = (const __nv_bfloat16*)d_x;
     if (ad) {
         uint8_t* w = (uint8_t*)d_work;
@@ -195,6 +196,22 @@ ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_
         }
     }
     return done(launch_project(p, sh, wk, d_W, n_sm, (cudaStream_t)stream), "project launch");
+}
+
+ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_t in_features, int32_t out_features,
+                             const void* d_A, const void* d_B, const float* d_scale, int32_t n_adapters, int32_t rank,
+                             const int32_t* d_ids, void* d_out, void* d_work, size_t work_bytes, void* stream) {
+    return project(d_x, n, d_W, in_features, out_features, d_A, d_B, d_scale, n_adapters, rank, d_ids, d_out, d_work, work_bytes,
+                   INT32_MAX, stream);
+}
+
+ds4moe_status ds4moe_selftest_project_wait(const void* d_x, int32_t n, const void* d_W, int32_t in_features, int32_t out_features,
+                                           const void* d_A, const void* d_B, const float* d_scale, int32_t n_adapters,
+                                           int32_t rank, const int32_t* d_ids, void* d_out, void* d_work, size_t work_bytes,
+                                           int32_t tiles, void* stream) {
+    if (tiles < 0) return fail(DS4MOE_ERR_ARG, "project: tiles %d", tiles);
+    return project(d_x, n, d_W, in_features, out_features, d_A, d_B, d_scale, n_adapters, rank, d_ids, d_out, d_work, work_bytes,
+                   tiles, stream);
 }
 
 ds4moe_status ds4moe_get_project_error(void* stream, int32_t* code) {

@@ -39,9 +39,32 @@ constexpr int kPSmemRows = 168 * 1024, kPSmemEntries = 150 * 1024;   // beside a
 // Error word of the projection's bounded waits, one per device.
 __device__ uint32_t g_project_err;
 
+// A bounded wait of the projection: false after kWaitNs (error bit 1), or when
+// another thread has given up.  Not in_time (the self-test's tiles): at once.
+//
+// What follows then, in both kernels: the thread sets the abort flag; the
+// producer issues no more and waits for its copies in flight, the issuing thread
+// for its MMAs; no accumulator is signalled as full that is not; the draining
+// warps go through all the tiles that are left and store NaN; a split tile's
+// CTAs look at one another's flags after their barrier, and store NaN if one is
+// set.
+__device__ __forceinline__ bool project_wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort, bool in_time) {
+    if (in_time) {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = global_ns();
+        do {
+            for (int i = 0; i < 16; ++i)
+                if (mbar_try_wait(bar, parity)) return true;
+            if (*abort) return false;
+        } while (global_ns() - t0 <= kWaitNs);
+    }
+    set_err(&g_project_err, kErrTimeout);
+    return false;
+}
+
 struct ProjSmem {
     uint64_t full[kPMaxStages], empty[kPMaxStages];
-    uint64_t accF[2], accE[2];
+    uint64_t accF[2], accE[2], last;
     uint32_t tmem;
     volatile uint32_t abort;
     int ahead[kAhead];
@@ -397,9 +420,11 @@ __device__ __forceinline__ void store16(const ProjectArgs& a, const uint32_t (&v
 // calling warp and its `warps` - 1 peers: the partial sums [bn][128] in the
 // shared memory (at `sums`) of ranks rank0, rank0 + step, .. of the cluster, in
 // that order.  A lane has four features, so that a warp's loads and stores are
-// wide and few enough to wait for.
-__device__ __forceinline__ void finish_split(const ProjectArgs& a, cg::cluster_group& cl, float* sums, int rank0, int step, int o,
-                                             int r0, int c0, int c1, int warp, int warps, int lane) {
+// wide and few enough to wait for.  NaN where a CTA of the cluster has given up.
+__device__ __forceinline__ void finish_split(const ProjectArgs& a, cg::cluster_group& cl, float* sums, volatile uint32_t* abort,
+                                             int ctas, int rank0, int step, int o, int r0, int c0, int c1, int warp, int warps,
+                                             int lane) {
+    const uint32_t bad = *const_cast<volatile uint32_t*>(cl.map_shared_rank(const_cast<uint32_t*>(abort), lane < ctas ? lane : 0));
     const float* part[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) part[p] = cl.map_shared_rank(sums, rank0 + (p < a.split ? p : 0) * step);
@@ -420,6 +445,7 @@ __device__ __forceinline__ void finish_split(const ProjectArgs& a, cg::cluster_g
                 }
             }
         }
+        if (__any_sync(0xffffffffu, bad)) v[0] = v[1] = v[2] = v[3] = __int_as_float(0x7fffffff);
         __nv_bfloat16* d = a.out + (size_t)(r0 + c) * a.fout + o;
         if (wide) {
             if (o + 4 * lane < a.fout)
@@ -433,7 +459,8 @@ __device__ __forceinline__ void finish_split(const ProjectArgs& a, cg::cluster_g
 }
 
 // A tile's accumulators (columns from taddr on) to out, with what the adapters
-// add to up to 64 rows (acc).  Not ok (a wait ran out): NaN.
+// add to up to 64 rows (acc).  Not ok (a wait ran out; the same for the whole
+// warp): NaN.
 template <bool Rows, int N>
 __device__ __forceinline__ void store_tile(const ProjectArgs& a, uint32_t taddr, int o, int lane, int r0, int rows, bool ok,
                                            const float (&acc)[N]) {
@@ -497,6 +524,7 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
             mbar_init(&S.accF[i], 1);
             mbar_init(&S.accE[i], 4);
         }
+        mbar_init(&S.last, 1);
         S.abort = 0;
         fence_barrier_init();
         // the first tile's first blocks are on their way before the others are set up
@@ -522,13 +550,17 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
     const bool one_block = 2 * R16 <= kPK;               // both pieces of t in one block
     const int per_entry = one_block ? 1 : 2 * ((R16 + kPK - 1) / kPK);
 
+    uint32_t blocks = 0;   // thread 0: copies sent
+
     if (warp == 0) {
         if (lane == 0) {
-            uint32_t it = 0;
-            bool waited = false;
+            const uint32_t sent = first < a.tiles ? min(a.stages, kb1 - kb0) : 0;   // above
+            uint32_t it = sent;
+            int use = 0;
+            bool waited = false, in_time = true;
             auto slot = [&]() -> int {
                 const int s = it % a.stages;
-                if (!mbar_wait(&S.empty[s], ((it / a.stages) & 1) ^ 1, err)) {
+                if (!project_wait(&S.empty[s], ((it / a.stages) & 1) ^ 1, &S.abort, in_time)) {
                     S.abort = 1;
                     return -1;
                 }
@@ -536,11 +568,10 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
                 ++it;
                 return s;
             };
-            for (int tile = first; tile < a.tiles && !S.abort; tile += step) {
+            for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
                 const int o0 = tile / a.row_tiles * kPM, rt = tile % a.row_tiles, r0 = rt * a.bn;
-                int kb = kb0;
-                if (tile == first) it = min(a.stages, kb1 - kb0), kb += it;   // sent above
-                for (; kb < kb1; ++kb) {
+                in_time = use < a.in_time;
+                for (int kb = kb0 + (tile == first ? (int)sent : 0); kb < kb1; ++kb) {
                     const int s = slot();
                     if (s < 0) break;
                     unsigned char* p = st + s * stage_bytes;
@@ -568,10 +599,7 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
                     }
                 }
             }
-            if (S.abort) {   // no copy may be in flight when the CTA leaves
-                const uint32_t n = it < (uint32_t)a.stages ? it : (uint32_t)a.stages;
-                for (uint32_t i = it - n; i < it; ++i) mbar_wait(&S.full[i % a.stages], (i / a.stages) & 1, err);
-            }
+            blocks = it;
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -580,14 +608,15 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
             bool waited = false;
             for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
                 const int rt = tile % a.row_tiles, buf = use & 1;
-                if (!mbar_wait(&S.accE[buf], ((use >> 1) & 1) ^ 1, err)) { S.abort = 1; break; }
+                const bool in_time = (int)use < a.in_time;
+                if (!project_wait(&S.accE[buf], ((use >> 1) & 1) ^ 1, &S.abort, in_time)) { S.abort = 1; break; }
                 tc_fence_after();
                 const uint32_t d = tmem + buf * a.bn;
                 uint32_t accumulate = 0;
                 // k steps [0, na) of the block's A against steps [b0, b0 + na) of its B
                 auto wait_full = [&]() -> int {
                     const int s = it % a.stages;
-                    if (!mbar_wait(&S.full[s], (it / a.stages) & 1, err)) { S.abort = 1; return -1; }
+                    if (!project_wait(&S.full[s], (it / a.stages) & 1, &S.abort, in_time)) { S.abort = 1; return -1; }
                     tc_fence_after();
                     ++it;
                     return s;
@@ -625,41 +654,43 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
                             umma_commit(&S.empty[s]);
                         }
                 }
+                if (S.abort) break;   // (this thread's own, or another's: the tile is not to look complete)
                 umma_commit(&S.accF[buf]);
             }
         }
     } else if (warp >= 4) {
         const int qd = warp & 3;   // TMEM lanes 32 qd .. 32 qd + 31
         uint32_t use = 0;
+        bool ok = true;   // the same for the whole warp; a phase behind one that was given up would look complete
         float* ts = reinterpret_cast<float*>(st + a.stages * stage_bytes);
         const int per = (a.bn + a.split - 1) / a.split, lo = per * rank_in;   // rows that this CTA of a split tile finishes
         const int mine = max(0, min(a.n, lo + per) - lo);                      // (Rows: there is one tile along the rows)
         if constexpr (Rows) stage_rows(a, ts, S.ids, lo, mine, tid - 128, 128);
-        for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
+        for (int tile = first; tile < a.tiles; tile += step, ++use) {
             const int buf = use & 1;
             const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + buf * a.bn;
             const int o = tile / a.row_tiles * kPM + 32 * qd + lane, r0 = tile % a.row_tiles * a.bn;
             const int rows = min(a.bn, a.n - r0);
             float acc[Rows ? kRowsMax : 1];
             if constexpr (Rows) adapter_rows(a, ts, S.ids, o, mine, acc);
-            if (!mbar_wait(&S.accF[buf], (use >> 1) & 1, err)) S.abort = 1;
-            const bool ok = !S.abort;   // a wait that ran out leaves NaN in the tile
+            ok = ok && __all_sync(0xffffffffu, project_wait(&S.accF[buf], (use >> 1) & 1, &S.abort, (int)use < a.in_time));
+            if (!ok) S.abort = 1;
             tc_fence_after();
-            if (a.split > 1) {
+            if (a.split > 1 && ok) {
                 float* part = reinterpret_cast<float*>(st) + 32 * qd + lane;   // [bn][128]; every stage is done with
                 for (int c0 = 0; c0 < a.bn; c0 += 16) {
                     uint32_t v[16];
                     tmem_ld_32x16(taddr + c0, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c0 + j) * kPM] = ok ? __uint_as_float(v[j]) : __int_as_float(0x7fffffff);
+                    for (int j = 0; j < 16; ++j) part[(c0 + j) * kPM] = __uint_as_float(v[j]);
                 }
                 if constexpr (Rows) {
 #pragma unroll
                     for (int j = 0; j < kRowsMax / 2; ++j)
                         if (j < mine) part[(lo + j) * kPM] += acc[j];
                 }
-            } else {
+            } else if (a.split == 1) {
                 store_tile<Rows>(a, taddr, o, lane, r0, rows, ok, acc);
             }
             tc_fence_before();
@@ -672,13 +703,23 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
         cg::cluster_group cl = cg::this_cluster();
         cl.sync();
         const int r0 = first % a.row_tiles * a.bn, per = (a.bn + a.split - 1) / a.split;
-        finish_split(a, cl, reinterpret_cast<float*>(st), 0, 1, first / a.row_tiles * kPM, r0, per * rank_in,
+        finish_split(a, cl, reinterpret_cast<float*>(st), &S.abort, a.split, 0, 1, first / a.row_tiles * kPM, r0, per * rank_in,
                      min(min(a.bn, a.n - r0), per * (rank_in + 1)), warp, kPThreads / 32, lane);
         cl.sync();   // peers have read this CTA's sums
     }
     if (Rows || a.counts) griddep_wait();   // this grid's end implies the first one's
     tc_fence_before();
     __syncthreads();
+    if (S.abort) {   // no copy and no MMA may be in flight when the CTA leaves
+        if (tid == 32) {   // the thread that issued the MMAs
+            umma_commit(&S.last);
+            mbar_wait(&S.last, 0, err);
+        } else if (tid == 0) {
+            const uint32_t n = min(blocks, (uint32_t)a.stages);
+            for (uint32_t i = blocks - n; i < blocks; ++i) mbar_wait(&S.full[i % a.stages], (i / a.stages) & 1, err);
+        }
+        __syncthreads();
+    }
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, acc_cols);
@@ -697,9 +738,10 @@ __global__ void __launch_bounds__(Rows ? 512 : kPThreads, 1) k_project(const __g
 // Split tiles as above: up to four pairs in a cluster, each a part of the K axis.
 struct PairSmem {
     uint64_t full[kPMaxStages], empty[kPMaxStages];
-    uint64_t accF, accE[2];
+    uint64_t accF, accE[2], last, gone;
     uint32_t tmem;
     volatile uint32_t abort;
+    uint32_t peer_blocks;   // of the leader: copies sent by the peer
     int ahead[kAhead];
     int ids[kRowsMax];
 };
@@ -767,6 +809,8 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
             mbar_init(&S.empty[i], 1);
         }
         mbar_init(&S.accF, 1);
+        mbar_init(&S.last, 1);
+        mbar_init(&S.gone, 1);
         for (int m = 0; m < 2; ++m) mbar_init(&S.accE[m], 8);
         S.abort = 0;
         fence_barrier_init();
@@ -784,13 +828,16 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
     const bool one_block = 2 * R16 <= kPK;
     const int per_entry = one_block ? 1 : 2 * ((R16 + kPK - 1) / kPK);
 
+    uint32_t blocks = 0;   // thread 0: copies sent by this CTA
+
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
-            bool waited = false;
+            int use = 0;
+            bool waited = false, in_time = true;
             auto slot = [&]() -> int {
                 const int s = it % a.stages;
-                if (!mbar_wait(&S.empty[s], ((it / a.stages) & 1) ^ 1, err)) {
+                if (!project_wait(&S.empty[s], ((it / a.stages) & 1) ^ 1, &S.abort, in_time)) {
                     stop();
                     return -1;
                 }
@@ -798,7 +845,8 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
                 ++it;
                 return s;
             };
-            for (int tile = first; tile < a.tiles && !S.abort; tile += step) {
+            for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
+                in_time = use < a.in_time;
                 const int o0 = tile / a.row_tiles * (4 * kPM) + r * kPM, rt = tile % a.row_tiles, r0 = rt * a.bn + r * half;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     const int s = slot();
@@ -830,10 +878,9 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
                     }
                 }
             }
-            if (S.abort && r == 0) {   // no copy of either CTA may be in flight when the pair leaves
-                const uint32_t n = it < (uint32_t)a.stages ? it : (uint32_t)a.stages;
-                for (uint32_t i = it - n; i < it; ++i) mbar_wait(&S.full[i % a.stages], (i / a.stages) & 1, err);
-            }
+            blocks = it;
+            if (r == 1)
+                asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(smem_addr(&S.peer_blocks), leader)), "r"(it) : "memory");
         }
     } else if (warp == 1) {
         if (lane == 0 && r == 0) {
@@ -842,18 +889,19 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
             bool waited = false;
             for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
                 const int rt = tile % a.row_tiles;
+                const bool in_time = (int)use < a.in_time;
                 uint32_t fresh = 3;   // accumulators not yet begun
                 auto block = [&](int na, int b0, bool again) -> bool {
                     const int s = it % a.stages;
                     if (!again) {
-                        if (!mbar_wait(&S.full[s], (it / a.stages) & 1, err)) { stop(); return false; }
+                        if (!project_wait(&S.full[s], (it / a.stages) & 1, &S.abort, in_time)) { stop(); return false; }
                         tc_fence_after();
                     }
                     const uint32_t p = smem_addr(st + s * stage_bytes);
                     const uint64_t db = umma_desc_sw128(p + 2 * kPStageA);
                     for (int m = 0; m < 2; ++m) {
                         if (fresh >> m & 1u) {   // the last tile's sums have been read
-                            if (!mbar_wait(&S.accE[m], (use & 1) ^ 1, err)) { stop(); return false; }
+                            if (!project_wait(&S.accE[m], (use & 1) ^ 1, &S.abort, in_time)) { stop(); return false; }
                             tc_fence_after();
                         }
                         const uint64_t da = umma_desc_sw128(p + m * kPStageA);
@@ -888,21 +936,23 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
                             next();
                         }
                 }
+                if (S.abort) break;   // (this thread's own, or another's: the tile is not to look complete)
                 pair_commit(&S.accF, leader);
             }
         }
     } else if (warp >= 4) {
         const int qd = warp & 3, m = (warp - 4) >> 2;   // TMEM lanes 32 qd .., accumulator m
         uint32_t use = 0;
+        bool ok = true;   // the same for the whole warp; a phase behind one that was given up would look complete
         float* ts = reinterpret_cast<float*>(st + a.stages * stage_bytes);
         if constexpr (Rows) stage_rows(a, ts, S.ids, 0, a.n, tid - 128, kPairThreads - 128);
-        for (int tile = first; tile < a.tiles && !S.abort; tile += step, ++use) {
+        for (int tile = first; tile < a.tiles; tile += step, ++use) {
             const int o = tile / a.row_tiles * (4 * kPM) + m * (2 * kPM) + r * kPM + 32 * qd + lane, r0 = tile % a.row_tiles * a.bn;
             const int rows = min(a.bn, a.n - r0);
             float acc[Rows ? kRowsMax : 1];
             if constexpr (Rows) adapter_rows(a, ts, S.ids, o, rows, acc);
-            if (!mbar_wait(&S.accF, use & 1, err)) stop();
-            const bool ok = !S.abort;
+            ok = ok && __all_sync(0xffffffffu, project_wait(&S.accF, use & 1, &S.abort, (int)use < a.in_time));
+            if (!ok && lane == 0) stop();
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + m * a.bn;
             if (a.split > 1) break;   // the sums meet below
@@ -922,7 +972,6 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
         for (int m = 0; m < 2; ++m) {
             if (warp >= 4 && (warp - 4) >> 2 == m) {
                 const int qd = warp & 3;
-                const bool ok = !S.abort;
                 float* part = reinterpret_cast<float*>(st) + 32 * qd + lane;   // [bn][128]
                 const uint32_t taddr = tmem + ((uint32_t)(32 * qd) << 16) + m * a.bn;
                 for (int c0 = 0; c0 < a.bn; c0 += 16) {
@@ -930,13 +979,13 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
                     tmem_ld_32x16(taddr + c0, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c0 + j) * kPM] = ok ? __uint_as_float(v[j]) : __int_as_float(0x7fffffff);
+                    for (int j = 0; j < 16; ++j) part[(c0 + j) * kPM] = __uint_as_float(v[j]);
                 }
             }
             __syncwarp();
             cl.sync();
-            finish_split(a, cl, reinterpret_cast<float*>(st), r, 2, first / a.row_tiles * (4 * kPM) + m * (2 * kPM) + r * kPM, r0,
-                         per * ks, c1, warp, kPairThreads / 32, lane);
+            finish_split(a, cl, reinterpret_cast<float*>(st), &S.abort, 2 * a.split, r, 2,
+                         first / a.row_tiles * (4 * kPM) + m * (2 * kPM) + r * kPM, r0, per * ks, c1, warp, kPairThreads / 32, lane);
             cl.sync();   // the peers have read this CTA's sums
         }
     }
@@ -944,6 +993,34 @@ __global__ void __launch_bounds__(Rows ? 512 : 640, 1)
     __syncwarp();
     tc_fence_before();
     cl.sync();   // neither CTA leaves while the other may still read its operands or signal its barriers
+    if (S.abort) {   // (the same in both CTAs by now)
+        // No copy and no MMA of either CTA may be in flight when the pair leaves.  All complete on the leader's barriers: it
+        // waits for its own and the peer's (an empty stage lets neither run ahead of the other by more than the stages), the
+        // peer for the leader.
+        if (r == 0 && tid == 32) {   // the thread that issued the MMAs
+            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(&S.last)) : "memory");
+            mbar_wait(&S.last, 0, err);
+        }
+        __syncthreads();
+        if (r == 0 && tid == 0) {
+            const uint32_t theirs = S.peer_blocks, all = max(blocks, theirs), n = min(all, (uint32_t)a.stages);
+            for (uint32_t i = all - n; i < all; ++i) {
+                uint64_t* bar = &S.full[i % a.stages];
+                if (i >= blocks)   // the peer's half alone
+                    mbar_arrive_expect_tx(bar, stage_bytes);
+                else if (i >= theirs)   // both are expected, the peer's half does not come
+                    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(stage_bytes)
+                                 : "memory");
+                mbar_wait(bar, (i / a.stages) & 1, err);
+            }
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_rank(smem_addr(&S.gone), leader + 1))
+                         : "memory");
+        } else if (tid == 0) {
+            bool gone = false;   // as long as the leader's waits may last
+            for (int k = 0; k < a.stages + 2 && !gone; ++k) gone = mbar_wait(&S.gone, 0, err);
+        }
+        __syncthreads();
+    }
     if (warp == 2) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");

@@ -267,8 +267,9 @@ ds4moe_status ds4moe_widen_rows(const void* d_q, int32_t q_format, const float* 
  * <= 2^20, rank a multiple of 8 in 8 .. 128, n_adapters <= 65536
  * (DS4MOE_ERR_SHAPE), n <= 2^20; x, W, A, B, out 16-byte aligned.  d_work: device scratch of at least
  * ds4moe_project_work_bytes bytes, 256-byte aligned, this call's alone until
- * it has run.  A bounded device-side wait that gives up leaves NaN in out and
- * sets the word that ds4moe_get_project_error reads. */
+ * it has run.  A bounded device-side wait (0.5 s) that gives up leaves NaN in
+ * every output that it kept from being computed and sets the word that
+ * ds4moe_get_project_error reads; the context stays usable. */
 ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_t in_features, int32_t out_features,
                              const void* d_A, const void* d_B, const float* d_scale, int32_t n_adapters, int32_t rank,
                              const int32_t* d_ids, void* d_out, void* d_work, size_t work_bytes, void* stream);
@@ -282,6 +283,15 @@ size_t ds4moe_project_work_bytes(int32_t n, int32_t in_features, int32_t out_fea
  * ds4moe_project into *code (0 = none, bit 1 = a bounded wait timed out, with
  * DS4MOE_ERR_TIMEOUT). */
 ds4moe_status ds4moe_get_project_error(void* stream, int32_t* code);
+
+/* Check of that failure path: ds4moe_project in which every wait of a CTA from
+ * its `tiles`-th tile of out on (0: the first) gives up at once.  Outputs of
+ * those tiles are NaN, the others' NaN or as ds4moe_project's; the error word is
+ * set.  Nothing faults, traps or hangs. */
+ds4moe_status ds4moe_selftest_project_wait(const void* d_x, int32_t n, const void* d_W, int32_t in_features,
+                                           int32_t out_features, const void* d_A, const void* d_B, const float* d_scale,
+                                           int32_t n_adapters, int32_t rank, const int32_t* d_ids, void* d_out,
+                                           void* d_work, size_t work_bytes, int32_t tiles, void* stream);
 
 /* The next token of each row of logits (n rows of `vocab` elements of `dtype`,
  * row_stride elements apart), by a given uniform number: with M the row's
@@ -451,7 +461,7 @@ ds4moe_status ds4moe_route_noalloc(ds4moe_t* h, const void* d_x, int32_t n_token
                                    float* d_weights, void* stream);
 
 /* Check of the failure path every bounded device-side wait takes: runs one
- * warp whose wait (the routine all the kernels' waits use) is on an mbarrier
+ * warp whose wait (the routine of the layer's kernels) is on an mbarrier
  * that nothing arrives at.  The wait gives up after its limit (0.5 s), sets
  * bit 1 of the workspace error word and the kernel returns, so the context
  * stays usable; ds4moe_get_device_error then returns DS4MOE_ERR_TIMEOUT.

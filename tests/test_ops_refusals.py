@@ -141,3 +141,9 @@ def test_binding_refuses_types_shapes_and_devices(lib):
     _refused("logits: unsupported type", m.ds4moe_sample, x.double(), _z(4), _z(4, dtype=torch.int32))
     _refused("next to each other", m.ds4moe_sample, _z(64, 4).t(), _z(4), _z(4, dtype=torch.int32))
     _refused("u: ", m.ds4moe_sample, x, _z(3), _z(4, dtype=torch.int32))
+
+
+def test_project_selftest_refuses_as_the_projection_does(lib):
+    assert lib.ds4moe_selftest_project_wait(A, 4, B, 64, 100, None, None, None, 0, 0, None, F, None, 0, -1, None) == ARG
+    assert lib.ds4moe_selftest_project_wait(A, 4, B, 60, 100, None, None, None, 0, 0, None, F, None, 0, 0, None) == SHAPE
+    assert lib.ds4moe_selftest_project_wait(A, 4, B, 64, 100, None, None, None, 0, 0, None, A, None, 0, 0, None) == ARG
