@@ -17,6 +17,8 @@
 #include <cooperative_groups.h>
 #include <cudaTypedefs.h>
 
+#include <mutex>
+
 #include "ops.cuh"
 #include "tcgen05.cuh"
 
@@ -36,8 +38,9 @@ constexpr int kRowsMin = 8, kRowsMax = 64;   // rows whose adapters the draining
 constexpr int kPSmem = 200 * 1024;       // of 227 KB
 constexpr int kPSmemRows = 168 * 1024, kPSmemEntries = 150 * 1024;   // beside a CTA of the first kernel
 
-// Error word of the projection's bounded waits, one per device.
-__device__ uint32_t g_project_err;
+// Error word of the projection's bounded waits, one per device, and where a
+// reader takes it to.
+__device__ uint32_t g_project_err, g_project_taken;
 
 // A bounded wait of the projection: false after kWaitNs (error bit 1), or when
 // another thread has given up.  Not in_time (the self-test's tiles): at once.
@@ -1177,11 +1180,20 @@ cudaError_t launch_project(ProjectArgs p, ShrinkArgs s, const ProjectWork& wk, c
     return cudaLaunchKernelEx(&cfg, kernel, mW, mX, mB, mT, p);
 }
 
+// One step reads and clears the word, so that an error set meanwhile on another
+// stream is in this answer or in the next.  One reader at a time has g_project_taken.
+static __global__ void k_take_project_error() { g_project_taken = atomicExch(&g_project_err, 0u); }
+
 cudaError_t read_project_error(uint32_t* code, cudaStream_t st) {
+    static std::mutex one;
+    const std::lock_guard<std::mutex> lock(one);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = cfg.blockDim = dim3(1);
+    cfg.stream = st;
     void* p = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&p, g_project_err);
+    cudaError_t e = cudaGetSymbolAddress(&p, g_project_taken);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_take_project_error);
     if (e == cudaSuccess) e = cudaMemcpyAsync(code, p, 4, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, 4, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     return e;
 }

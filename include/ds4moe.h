@@ -279,9 +279,10 @@ ds4moe_status ds4moe_project(const void* d_x, int32_t n, const void* d_W, int32_
 size_t ds4moe_project_work_bytes(int32_t n, int32_t in_features, int32_t out_features, int32_t n_adapters,
                                  int32_t rank);
 
-/* Synchronize `stream`, then read and clear the current device's error word of
- * ds4moe_project into *code (0 = none, bit 1 = a bounded wait timed out, with
- * DS4MOE_ERR_TIMEOUT). */
+/* Read and clear, behind what is on `stream` and in one step, the current
+ * device's error word of ds4moe_project into *code (0 = none, bit 1 = a bounded
+ * wait timed out, with DS4MOE_ERR_TIMEOUT), and synchronize `stream`.  One word
+ * serves all streams of the device. */
 ds4moe_status ds4moe_get_project_error(void* stream, int32_t* code);
 
 /* Check of that failure path: ds4moe_project in which every wait of a CTA from

@@ -86,3 +86,19 @@ def test_no_wait_gives_up_in_time():
     m.ds4moe_project(out=a, **d)
     m.ds4moe_selftest_project_wait(out=b, tiles=1000, **d)
     assert torch.equal(a, b) and _error() == (0, 0)
+
+
+def test_error_word_is_taken_in_one_step():
+    """Reads on one stream while projections that give up run on another: every error is in some answer."""
+    d = _data(8, 512, 640, 0, 0)
+    out = torch.empty(8, 640, dtype=BF16, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    seen = 0
+    for _ in range(50):
+        m.ds4moe_selftest_project_wait(out=out, stream=side, **d)
+        seen += _error()[1] == 2
+        side.synchronize()
+        seen += _error()[1] == 2
+        assert seen >= 1
+        seen = 0
