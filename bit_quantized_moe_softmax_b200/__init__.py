@@ -404,14 +404,16 @@ def ds4moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residu
     n, H = x.shape
     dev = x.get_device()
     shape = (n, H)
+    groups = 1 if q is None and scale is None else _q8_groups(where, group, H)   # (group means nothing without codes)
     _tensors(where, dev, (
         ("x", x, shape, _ACT), ("weight", weight, (H,), (torch.float32,)), ("residual", residual, shape, _ACT),
         ("sum", sum, shape, _ACT if residual is None else (residual.dtype,)), ("out", out, shape, _ACT),
         ("q", q, shape, _Q8),
-        ("scale", scale, (n, _q8_groups(where, group, H)), (torch.float32,))))
+        ("scale", scale, (n, groups), (torch.float32,))))
     _call(where, dev, stream, lib().ds4moe_add_rmsnorm, x.data_ptr(), _ACT[x.dtype], _ptr(residual),
           0 if residual is None else _ACT[residual.dtype], weight.data_ptr(), eps, n, H, _ptr(sum), _ptr(out),
-          0 if out is None else _ACT[out.dtype], _ptr(q), 0 if q is None else _Q8[q.dtype], group, _ptr(scale))
+          0 if out is None else _ACT[out.dtype], _ptr(q), 0 if q is None else _Q8[q.dtype], 0 if q is None else group,
+          _ptr(scale))
 
 
 def ds4moe_widen_rows(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, group: int = 128, stream=None):

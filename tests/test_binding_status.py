@@ -52,3 +52,12 @@ def test_done_and_not_in_order(monkeypatch, which):
         monkeypatch.setattr(m, "_tensors", lambda *args: None)
         call()
         assert seen == long_way
+
+
+def test_group_means_nothing_without_codes():
+    """Refused for being no CUDA tensors, and not for a group that nothing uses."""
+    x = torch.zeros(2, 64)
+    with pytest.raises(m.Ds4MoeError, match="CUDA"):
+        m.ds4moe_add_rmsnorm(x, x[0], 1e-6, out=x.clone(), group=48)
+    with pytest.raises(m.Ds4MoeError, match="group"):
+        m.ds4moe_add_rmsnorm(x, x[0], 1e-6, q=x.to(torch.int8), scale=x[:, :2].contiguous(), group=48)
