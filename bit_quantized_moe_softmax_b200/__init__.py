@@ -338,6 +338,16 @@ def _refuse(where: str, msg: str):
     raise Ds4MoeError(-1, where, msg)
 
 
+def _fits(*sizes: int) -> bool:
+    """Whether the C entry points' 32-bit sizes hold these (ctypes would cut them off)."""
+    return all(-1 << 31 <= s < 1 << 31 for s in sizes)
+
+
+def _sizes(where: str, *sizes: int):
+    if not _fits(*sizes):
+        _refuse(where, "sizes %s: one is beyond 32 bits" % (sizes,))
+
+
 def _tensors(where: str, dev: int, specs):
     """Each (name, tensor or None, shape, types): on CUDA device dev, contiguous, of that shape and one of the types."""
     for _, t, shape, types in specs:
@@ -402,6 +412,7 @@ def ds4moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, residu
     if x.dim() != 2:
         _refuse(where, "x: %d dimensions, expected [n, hidden]" % x.dim())
     n, H = x.shape
+    _sizes(where, n, H)
     dev = x.get_device()
     shape = (n, H)
     groups = 1 if q is None and scale is None else _q8_groups(where, group, H)   # (group means nothing without codes)
@@ -426,6 +437,7 @@ def ds4moe_widen_rows(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, g
     if q.dim() != 2:
         _refuse(where, "q: %d dimensions, expected [n, hidden]" % q.dim())
     n, H = q.shape
+    _sizes(where, n, H)
     dev = q.get_device()
     _tensors(where, dev, (("q", q, (n, H), _Q8),
                                ("scale", scale, (n, _q8_groups(where, group, H)), (torch.float32,)),
@@ -435,7 +447,8 @@ def ds4moe_widen_rows(q: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, g
 
 
 def ds4moe_project_work_bytes(n: int, in_features: int, out_features: int, n_adapters: int, rank: int) -> int:
-    return lib().ds4moe_project_work_bytes(n, in_features, out_features, n_adapters, rank)
+    sizes = (n, in_features, out_features, n_adapters, rank)
+    return lib().ds4moe_project_work_bytes(*sizes) if _fits(*sizes) else 0
 
 
 def ds4moe_project(x: torch.Tensor, W: torch.Tensor, out: torch.Tensor, A: torch.Tensor | None = None,
@@ -469,6 +482,7 @@ def _project(where, fn, x, W, out, A, B, adapter_scale, ids, work, stream, *more
         na, rank = A.shape[0], A.shape[1]
     elif B is not None or adapter_scale is not None or ids is not None:
         _refuse(where, "B, adapter_scale and ids need A")
+    _sizes(where, n, fin, fout, na, rank)
     _tensors(where, dev, (("x", x, (n, fin), bf), ("W", W, (fout, fin), bf), ("out", out, (n, fout), bf),
                                ("A", A, (na, rank, fin), bf), ("B", B, (na, fout, rank), bf),
                                ("adapter_scale", adapter_scale, (na,), (torch.float32,)),
@@ -499,6 +513,7 @@ def ds4moe_get_project_error(stream=None) -> int:
 
 def ds4moe_selftest_project_wait(x, W, out, A=None, B=None, adapter_scale=None, ids=None, tiles: int = 0, stream=None):
     """ds4moe_project whose waits give up at once from each CTA's ``tiles``-th tile on: NaN there, and the error word."""
+    _sizes("ds4moe_selftest_project_wait", tiles)
     _project("ds4moe_selftest_project_wait", lib().ds4moe_selftest_project_wait, x, W, out, A, B, adapter_scale, ids, None,
              stream, tiles)
 
@@ -520,6 +535,7 @@ def ds4moe_sample(logits: torch.Tensor, u: torch.Tensor, token: torch.Tensor, te
     if logits.dim() != 2:
         _refuse(where, "logits: %d dimensions, expected [n, vocab]" % logits.dim())
     n, V = logits.shape
+    _sizes(where, n, V)
     dev = logits.get_device()
     if logits.dtype not in _ACT:
         _refuse(where, "logits: unsupported type %s" % logits.dtype)

@@ -61,3 +61,25 @@ def test_group_means_nothing_without_codes():
         m.ds4moe_add_rmsnorm(x, x[0], 1e-6, out=x.clone(), group=48)
     with pytest.raises(m.Ds4MoeError, match="group"):
         m.ds4moe_add_rmsnorm(x, x[0], 1e-6, q=x.to(torch.int8), scale=x[:, :2].contiguous(), group=48)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """2^32 + 4 rows are not 4 rows (tensors without memory stand in)."""
+    def z(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    n, bf, i32 = 2 ** 32 + 4, torch.bfloat16, torch.int32
+    for call in (lambda: m.ds4moe_add_rmsnorm(z(n, 64), z(64), 1e-6, out=z(n, 64)),
+                 lambda: m.ds4moe_add_rmsnorm(z(4, n), z(n), 1e-6, out=z(4, n)),
+                 lambda: m.ds4moe_widen_rows(z(n, 64, dtype=torch.int8), z(n, 1), z(n, 64)),
+                 lambda: m.ds4moe_project(z(n, 64, dtype=bf), z(8, 64, dtype=bf), z(n, 8, dtype=bf)),
+                 lambda: m.ds4moe_project(z(4, 64, dtype=bf), z(n, 64, dtype=bf), z(4, n, dtype=bf)),
+                 lambda: m.ds4moe_project(z(4, 64, dtype=bf), z(8, 64, dtype=bf), z(4, 8, dtype=bf), A=z(n, 8, 64, dtype=bf),
+                                          B=z(n, 8, 8, dtype=bf), adapter_scale=z(n), ids=z(4, dtype=i32)),
+                 lambda: m.ds4moe_sample(z(n, 64), z(n), z(n, dtype=i32)), lambda: m.ds4moe_sample(z(4, n), z(4), z(4, dtype=i32))):
+        with pytest.raises(m.Ds4MoeError, match="32 bits") as e:
+            call()
+        assert e.value.status == -1
+    assert m.ds4moe_project_work_bytes(4, 64, 100, 3, 8) > 0
+    for bad in ((n, 64, 100, 3, 8), (4, 2 ** 32 + 64, 100, 3, 8), (4, 64, 100, 2 ** 32 + 3, 8), (4, 64, 100, 3, 2 ** 32 + 8)):
+        assert m.ds4moe_project_work_bytes(*bad) == 0
