@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -311,7 +312,7 @@ _Q8 = {torch.float8_e4m3fn: DS4MOE_Q8_E4M3, torch.int8: DS4MOE_Q8_INT8}
 
 
 class _NoFast:
-    """In place of _fastcall.so where it was not built: every call goes the long way."""
+    """In place of _fastcall where it was not built, or cannot be loaded: every call goes the long way."""
     add_rmsnorm = widen_rows = project = sample = staticmethod(lambda *args: False)
 
 
@@ -319,18 +320,23 @@ _fast = None
 
 
 def _load_fast():
-    """_fastcall.so: checks and call in one step for tensors of the current device on its current stream: True, or
+    """_fastcall: checks and call in one step for tensors of the current device on its current stream: True, or
     False (and nothing launched) where a call is not plainly in order, or the status of one that failed behind its
     checks and so is not made again."""
     global _fast
-    path = os.path.join(_PKG, "_fastcall.so")
+    from .build import fast_path
+
+    path, found = fast_path(), _NoFast
     if os.path.exists(path):
         lib()  # the library that it calls
-        spec = importlib.util.spec_from_file_location("_fastcall", path)
-        _fast = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_fast)
-    else:
-        _fast = _NoFast
+        try:
+            spec = importlib.util.spec_from_file_location("_fastcall", path)
+            found = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(found)
+        except ImportError as e:
+            warnings.warn("%s: %s; the calls that it shortens check in Python" % (os.path.basename(path), e))
+            found = _NoFast
+    _fast = found
     return _fast
 
 

@@ -1,10 +1,11 @@
-"""Build libds4moe.so (the C ABI of include/ds4moe.h) for sm_100a with nvcc, in-tree, and _fastcall.so, the Python
-binding's short way to some of its calls (csrc/fastcall.cpp), against torch's headers."""
+"""Build libds4moe.so (the C ABI of include/ds4moe.h) for sm_100a with nvcc, in-tree, and the Python binding's
+short way to some of its calls (csrc/fastcall.cpp), against torch's headers."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -12,7 +13,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libds4moe.so")
 FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
-FAST = os.path.join(PKG, "_fastcall.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared"]
 
@@ -33,12 +33,20 @@ def stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def fast_path() -> str:
+    """Of the Python and the torch that it is built against, so that no other's is loaded."""
+    import torch
+
+    return os.path.join(PKG, "_fastcall.%s-torch%s.so" % (sys.implementation.cache_tag, torch.__version__))
+
+
 def build_fast(force: bool = False) -> str | None:
-    """_fastcall.so; None (and no such file) where it cannot be built: the binding then checks in Python."""
+    """The file at fast_path(); None (and no such file) where it cannot be built: the binding then checks in Python."""
     header = os.path.join(ROOT, "include", "ds4moe.h")
-    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= max(map(os.path.getmtime, (FAST_SRC, header, __file__))):
-        return FAST
-    tmp = FAST + ".tmp%d" % os.getpid()
+    fast = fast_path()
+    if not force and os.path.exists(fast) and os.path.getmtime(fast) >= max(map(os.path.getmtime, (FAST_SRC, header, __file__))):
+        return fast
+    tmp = fast + ".tmp%d" % os.getpid()
     try:
         import torch
         from torch.utils import cpp_extension
@@ -51,14 +59,14 @@ def build_fast(force: bool = False) -> str | None:
                                "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi()),
                                *["-I" + i for i in includes], FAST_SRC, "-o", tmp, "-L" + libs, "-ltorch_python", "-ltorch",
                                "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libds4moe.so", "-Wl,-rpath,$ORIGIN"])
-        os.replace(tmp, FAST)
+        os.replace(tmp, fast)
     except (OSError, ImportError, subprocess.CalledProcessError) as e:
-        print("_fastcall.so was not built: %s" % e)
-        for p in (tmp, FAST):
+        print("%s was not built: %s" % (os.path.basename(fast), e))
+        for p in (tmp, fast):
             if os.path.exists(p):
                 os.remove(p)
         return None
-    return FAST
+    return fast
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:

@@ -1,6 +1,9 @@
 """The binding of the operators around the layer, without a GPU: what becomes of the
 short way's answer."""
+import os
+import sys
 import types
+import warnings
 
 import pytest
 import torch
@@ -83,3 +86,34 @@ def test_sizes_beyond_32_bits_are_refused():
     assert m.ds4moe_project_work_bytes(4, 64, 100, 3, 8) > 0
     for bad in ((n, 64, 100, 3, 8), (4, 2 ** 32 + 64, 100, 3, 8), (4, 64, 100, 2 ** 32 + 3, 8), (4, 64, 100, 3, 2 ** 32 + 8)):
         assert m.ds4moe_project_work_bytes(*bad) == 0
+
+
+# ------------------------------------------------------------------ the compiled way's file
+def test_compiled_way_is_of_this_python_and_torch(monkeypatch):
+    from bit_quantized_moe_softmax_b200 import build
+
+    path = build.fast_path()
+    assert torch.__version__ in path and sys.implementation.cache_tag in path and path.endswith(".so")
+    assert os.path.exists(path)
+    monkeypatch.setattr(m, "_fast", None)
+    assert m._load_fast() is not m._NoFast and m._fast.add_rmsnorm() is False
+    monkeypatch.setattr(torch, "__version__", "0.0")   # another torch: its file is not there, this one's is not loaded
+    monkeypatch.setattr(m, "_fast", None)
+    assert build.fast_path() != path and m._load_fast() is m._NoFast
+
+
+@pytest.mark.parametrize("content", [b"", b"no library", b"\x7fELF" + bytes(200)])
+def test_a_file_that_does_not_load_leaves_the_long_way(monkeypatch, tmp_path, content):
+    from bit_quantized_moe_softmax_b200 import build
+
+    path = tmp_path / "_fastcall.so"
+    path.write_bytes(content)
+    monkeypatch.setattr(build, "fast_path", lambda: str(path))
+    monkeypatch.setattr(m, "_fast", None)
+    x = torch.zeros(2, 8)
+    with pytest.warns(UserWarning, match="check in Python"), pytest.raises(m.Ds4MoeError, match="CUDA"):
+        m.ds4moe_add_rmsnorm(x, x[0], 1e-6, out=x.clone())
+    with warnings.catch_warnings():   # said once
+        warnings.simplefilter("error")
+        with pytest.raises(m.Ds4MoeError, match="CUDA"):
+            m.ds4moe_widen_rows(x.to(torch.int8), x[:, :1].contiguous(), x.clone())
