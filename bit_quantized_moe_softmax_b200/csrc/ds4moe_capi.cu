@@ -813,6 +813,8 @@ ds4moe_status ds4moe_probe(ds4moe_t* h, int32_t plan, int32_t which, int32_t e, 
     if (n < 1 || n > (1 << 20)) return fail(DS4MOE_ERR_ARG, "probe: n_rows %d outside 1..2^20", n);
     if (!d_in || !d_out) return fail(DS4MOE_ERR_ARG, "probe: NULL buffer");
     if (!aligned16(d_in) || !aligned16(d_out)) return fail(DS4MOE_ERR_ALIGN, "probe: buffers must be 16-byte aligned");
+    if (plan == 1 && ((uintptr_t)d_out & 31))   // the GEMM's epilogue stores 32 bytes at a time
+        return fail(DS4MOE_ERR_ALIGN, "probe: the prefill plan's out must be 32-byte aligned");
     std::string why;
     if (!h->ready(&why)) return fail(DS4MOE_ERR_NOT_READY, "probe: %s", why.c_str());
     if (e < -1 || e >= h->D.E) return fail(DS4MOE_ERR_ARG, "probe: expert %d out of range", e);

@@ -419,7 +419,8 @@ ds4moe_status ds4moe_dequant(ds4moe_t* h, int32_t e, int32_t which, int32_t as_b
  *     grouped GEMM.  which 0: d_in = activations [n][H] bfloat16, d_out =
  *     [n][2I] binary32, gate accumulators then up accumulators (no SwiGLU);
  *     which 2: d_in = h [n][I] bfloat16, d_out = [n][H] binary32.
- * d_in and d_out are 16-byte aligned device buffers; n in 1..2^20 (plan 1).
+ * d_in and d_out are 16-byte aligned device buffers, d_out of plan 1 32-byte
+ * aligned; n in 1..2^20 (plan 1).
  * Uses the workspace of the plan (its routing and intermediates are
  * overwritten). */
 ds4moe_status ds4moe_probe(ds4moe_t* h, int32_t plan, int32_t which, int32_t e, const void* d_in, int32_t n_rows,
