@@ -92,7 +92,7 @@ struct Weigh {
 
     // before the row's maximum is known
     __device__ __forceinline__ void set_temperature(float T, const double* table) {
-        c = fmin(kTab * 1.44269504088896340736 / (double)T, 1e38);
+        c = fmin(kTab * 1.44269504088896340736 / (double)T, 1e38);   // (1e38: for set_maximum, which lowers such a c)
         reach = fmax(8192.0 / (kTab * 1.44269504088896340736) * (double)T, 8192e-38);   // 8192 / c
         tab = table;
     }
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
     float P = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
     if (!(T > 0.f)) T = 1.f, K = 1, P = 1.f, mp = 0.f, u = 0.f;   // greedy: the first token of the order
 
-    const double inv = 1.0 / (double)T;
+    double inv = 1.0 / (double)T;
     Weigh weigh;
     weigh.set_temperature(T, S.tab);
 
@@ -359,6 +359,15 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
         for (int i = tid; i < kSW * a.seg; i += kST) vals[i] = vals[i] == INFINITY ? 0.f : kNegInf;
         mx = 0.f;
         own_max = own_max == INFINITY ? 0.f : kNegInf;
+        __syncthreads();
+    } else if (T < 0x1p-96f && fabsf(mx) < 0x1p30f) {
+        // 1 / T is beyond binary32, and tokens a step apart may share the weight: logits and temperature by 2^96 (what
+        // overflows is further below the maximum than has a weight)
+        for (int i = tid; i < kSW * a.seg; i += kST) vals[i] *= 0x1p96f;
+        mx *= 0x1p96f;
+        own_max *= 0x1p96f;
+        inv *= 0x1p-96;
+        weigh.set_temperature(T * 0x1p96f, S.tab);
         __syncthreads();
     }
     const bool by_k = K >= 1 && K < a.V, by_p = P < 1.f, by_m = mp > 0.f;

@@ -60,3 +60,18 @@ def test_order_of_tiny_logits_beside_a_huge_one():
     l[:, 0] = torch.tensor([2e37, 3e38, 1.0])
     for k in (3, 40):
         _check(l, torch.tensor([0.999, 0.999, 0.5]), T=float("inf"), k=k)
+
+
+@pytest.mark.parametrize("T", [1e-45, 3e-42, 1e-38, 2e-37, 1e-33, 1e-29, 2e-29])
+@pytest.mark.parametrize("V", [13, 700, 20000])
+def test_tiny_temperatures_of_tiny_logits(T, V):
+    """Only (l - M) / T counts: logits of the temperature's own size share the weight, down to binary32's last steps;
+    beside them tokens that are far below, and a maximum far above."""
+    l = torch.randn(4, V, generator=torch.Generator().manual_seed(V), dtype=torch.float64) * 2
+    l = (l * float(torch.tensor(T))).float()
+    l[1, ::3] = -1e5
+    l[2, 1::4] = torch.finfo(torch.float32).min
+    l[3, V // 2] = 1e12
+    u = torch.tensor([0.1, 0.5, 0.9, 0.7])
+    for f in (dict(), dict(k=9), dict(p=0.8), dict(k=V - 2, p=0.9, mp=0.01)):
+        _check(l, u, T=T, **f)
