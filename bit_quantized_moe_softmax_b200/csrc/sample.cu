@@ -73,6 +73,11 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
+// The largest binary32 value below a finite one (not -0).
+__device__ __forceinline__ float next_below(float m) {
+    return __uint_as_float(m > 0.f ? __float_as_uint(m) - 1 : m < 0.f ? __float_as_uint(m) + 1 : 0x80000001u);
+}
+
 // exp((l - M) / T) of one token in binary64: 2^(y / 128), y = (l - M) 128
 // log2(e) / T, from a table of 2^(j / 128) and four terms of the series of
 // 2^(r / 128), |r| <= 1/2 (a little more, as binary32 finds the nearest
@@ -97,7 +102,7 @@ struct Weigh {
         tab = table;
     }
     __device__ __forceinline__ void set_maximum(float m) {
-        const float below = __uint_as_float(m > 0.f ? __float_as_uint(m) - 1 : m < 0.f ? __float_as_uint(m) + 1 : 0x80000001u);
+        const float below = next_below(m);
         // a power of two (2^104 at the lowest value), and 1 / step by its exponent
         const double step = below == kNegInf ? 0x1p104 : (double)m - (double)below;
         const double most = 6000.0 * __hiloint2double(0x7fe00000 - __double2hiint(step), 0);
@@ -275,6 +280,9 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
     int K = a.top_k ? a.top_k[row] : 0;
     float P = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? a.min_p[row] : 0.f, u = a.u[row];
     if (!(T > 0.f)) T = 1.f, K = 1, P = 1.f, mp = 0.f, u = 0.f;   // greedy: the first token of the order
+    // min-p from 1 on: the tokens at the maximum alone, whatever else has a weight that rounds to 1 (at T infinite all
+    // weigh 1, and are kept)
+    if (mp >= 1.f) mp = T < INFINITY ? 1.f : 0.5f;
 
     double inv = 1.0 / (double)T;
     Weigh weigh;
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
         __syncthreads();
     }
     const bool by_k = K >= 1 && K < a.V, by_p = P < 1.f, by_m = mp > 0.f;
-    const double minw = fmin((double)mp, 1.0);
+    const double minw = (double)mp;
     weigh.set_maximum(mx);
     const int s0 = warp * a.seg;   // this warp's tokens: s0 .. s0 + seg - 1
 
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
             __syncthreads();
         }
         // (what follows the last token with a weight is not in: the first one always is)
-        const bool in = units && inc - units < target && (tid == 0 || !(by_m && w < minw));
+        const bool in = units && inc - units < target && (tid == 0 || !(by_m && (w < minw || (mp == 1.f && l < mx))));
         const int m = __syncthreads_count(in);   // a prefix
         if (tid == m - 1) S.list[0] = v, S.list[1] = inc;
         __syncthreads();
@@ -687,6 +695,8 @@ __global__ void __launch_bounds__(kST, C == 16 ? 1 : 2) k_sample(SampleArgs a) {
             __syncwarp();
         }
     }
+
+    if (!small && mp == 1.f && thr < mx) thr = next_below(mx), last = -1;
 
     // weights of this lane's four tokens from i on, those that are kept
     auto kept = [&](int i, double (&w)[4]) {

@@ -236,7 +236,8 @@ ds4moe_status ds4moe_combine_slots(const float* d_y, const float* d_w, const flo
  * 8-bit codes of q_format with d_scale [n][ceil(hidden / group)] binary32
  * (group 32, 64 or 128 columns; group 0: one scale per row, [n]): scale =
  * max|y| of the group / 448 (e4m3) or / 127 (int8), code = y / scale rounded
- * to nearest even; a group of zeros has scale 0 and codes 0, a group with a
+ * to nearest even and no larger than the format holds (a scale below 2^-126 may
+ * have been rounded down); a group whose scale is 0 has codes 0, a group with a
  * value that is not finite widens to NaN.  hidden <= 16384 (DS4MOE_ERR_SHAPE);
  * eps positive and finite; d_x, d_residual, d_weight, d_sum, d_out and d_q
  * 16-byte aligned. */
@@ -299,7 +300,8 @@ ds4moe_status ds4moe_selftest_project_wait(const void* d_x, int32_t n, const voi
  * largest logit and w_i = exp((l_i - M) / T), the tokens ordered by (logit
  * descending, index ascending),
  *   top-k keeps the first k; top-p the shortest prefix whose w sum to at least
- *   p of the top-k set's; min-p the tokens with w >= min_p (w = 1 for M);
+ *   p of the top-k set's; min-p the tokens with w >= min_p (w = 1 for M; a
+ *   min_p above 1 counts as 1, and 1 keeps the tokens at M alone);
  * token = the first kept one, in index order, whose running sum of w exceeds u
  * times the kept total.  d_temperature, d_top_k, d_top_p, d_min_p: one value
  * per row, or NULL for off.  T <= 0 (or NaN) is greedy: the first token of the

@@ -75,3 +75,40 @@ def test_tiny_temperatures_of_tiny_logits(T, V):
     u = torch.tensor([0.1, 0.5, 0.9, 0.7])
     for f in (dict(), dict(k=9), dict(p=0.8), dict(k=V - 2, p=0.9, mp=0.01)):
         _check(l, u, T=T, **f)
+
+
+@pytest.mark.parametrize("V", [20, 900, 40000])
+@pytest.mark.parametrize("f", [dict(), dict(top_k=7), dict(top_k=700), dict(top_p=0.9), dict(top_k=15, top_p=0.9999)])
+@pytest.mark.parametrize("T", [1.0, 1e16, 3e38])
+def test_min_p_of_one_keeps_the_maximum_alone(V, f, T):
+    """Tokens whose weight rounds to 1 in binary64 without being at the maximum are not kept."""
+    n = 3
+    l = torch.zeros(n, V) if T > 1 else torch.full((n, V), 1e-18)
+    l[:, 5::2] = -1e-17 if T == 1 else -0.5
+    l[0, 9], l[1, [7, 11]] = (1e-17, 2e-17) if T == 1 else (0.25, 0.5)
+    l[2] = torch.finfo(torch.float32).min
+    at = [[9], [7, 11], list(range(V))]
+    p = {k: torch.full((n,), v, dtype=torch.int32 if k == "top_k" else torch.float32, device="cuda") for k, v in f.items()}
+    token, prob, probs = torch.empty(n, dtype=torch.int32, device="cuda"), torch.empty(n, device="cuda"), torch.empty(n, V, device="cuda")
+    u = torch.tensor([0.99, 0.25, 0.0], device="cuda")
+    m.ds4moe_sample(l.cuda(), u, token, temperature=torch.full((n,), T, device="cuda"), min_p=torch.ones(n, device="cuda"),
+                    prob=prob, probs=probs, **p)
+    for i in range(n):
+        kept = at[i]
+        if i == 2:   # all alike: top-k's or top-p's share of them, from the lowest index on
+            kept = kept[:f.get("top_k", V)]
+            if "top_p" in f:
+                kept = kept[:int((probs[i] > 0).sum())]
+                assert abs(len(kept) / min(V, f.get("top_k", V)) - f["top_p"]) <= 1.0 / len(kept)
+        want = torch.zeros(V)
+        want[kept] = 1.0 / len(kept)
+        assert int(token[i]) in kept and torch.allclose(probs[i].cpu(), want, rtol=2.0 ** -22, atol=0), i
+        assert int(token[i]) == kept[int(float(u[i]) * len(kept))]
+
+
+def test_min_p_of_one_at_an_infinite_temperature():
+    """exp((l - M) / T) is 1 for every finite logit there, and 1 >= 1."""
+    l = torch.randn(2, 500, generator=torch.Generator().manual_seed(1))
+    l[0, ::4] = -float("inf")
+    for f in (dict(), dict(k=40), dict(p=0.5)):
+        _check(l, torch.tensor([0.3, 0.8]), T=float("inf"), mp=1.0, **f)
