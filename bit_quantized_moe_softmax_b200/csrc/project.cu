@@ -345,8 +345,9 @@ static cudaError_t shrink_launch(const ShrinkArgs& s, dim3 grid, cudaStream_t st
 // adapters): a block of the K axis per adapter would be zero but for a row or
 // two, so the warps that drain the accumulators add the adapters themselves, in
 // binary32, while the MMAs run: a lane has one output feature and reads its
-// `rank` values of B for each row (a warp: consecutive memory), eight rows' loads
-// in flight.  Of a split tile each CTA adds and stages the rows that it finishes.
+// `rank` values of B for each row, 16 bytes at a time (the warp's 32 features lie
+// next to each other, so all of a row's lines are used), eight rows' loads in
+// flight.  Of a split tile each CTA adds and stages the rows that it finishes.
 // acc[i] += B[id][o] . t for the first `rows` of the CTA's rows; ts, ids: their t
 // [rows][rank] and adapters (or -1) in shared memory.
 __device__ __forceinline__ void adapter_rows(const ProjectArgs& a, const float* ts, const int* ids, int o, int rows,
@@ -1063,7 +1064,7 @@ static cudaError_t encode(CUtensorMap* map, const void* base, uint64_t cols, uin
 // its operands, 33 bytes a clock with all SMs reading (128 bytes per feature
 // and row; the MMAs take less at every size here); a round of tiles some more
 // clocks for its start and end, above all the pairs' epilogue.
-// 4096 x 4096 x 4096: pairs of 240 rows, two rounds, 101 us; single CTAs 174 us.
+// 4096 x 4096 x 4096: pairs of 240 rows, two rounds, 102 us; single CTAs 174 us.
 // 500 x 2056 x 5001: single CTAs of 176 rows, 26 us; pairs of 80 rows 31 us.
 static void project_tile(int n, int fin, int fout, ProjectWork& w) {
     constexpr int64_t n_sm = 148;   // the size of the work buffer must not depend on the current device

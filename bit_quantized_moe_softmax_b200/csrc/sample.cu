@@ -21,9 +21,10 @@
 // where there are more than 512 (logits of few bits have many ties), counted
 // over their keys' bits.  Where all tokens down to that bin are at most 512,
 // they are sorted together and the remaining filters and the draw need no
-// other.  131,072 binary32 logits: one row 9 us without filters, 15 with all;
-// 256 rows 104 us without, 290 with top-p (7 % of HBM's rate: what bounds them
-// is the issue of some 70 to 160 instructions per 32 tokens).
+// other.  131,072 binary32 logits: one row 8 us without filters, 15 with all;
+// 256 rows 109 us without, 292 with top-p (7 % of HBM's rate).  No unit is full
+// there (issue slots 56 %, ALU 41 %, the shared-memory pipe 42 %): seven warps per
+// scheduler wait for dependent instructions, shared memory and barriers.
 #include <cooperative_groups.h>
 
 #include "ds4moe_internal.cuh"
@@ -81,9 +82,9 @@ __device__ __forceinline__ float next_below(float m) {
 // exp((l - M) / T) of one token in binary64: 2^(y / 128), y = (l - M) 128
 // log2(e) / T, from a table of 2^(j / 128) and four terms of the series of
 // 2^(r / 128), |r| <= 1/2 (a little more, as binary32 finds the nearest
-// integer): the fifth is below 2e-15, a twentieth of the unit 2^-44.  What
-// bounds the passes over the weights is the issue of their instructions, so
-// every one counts: the integer n comes from a binary32 addition and is used
+// integer): the fifth is below 2e-15, a twentieth of the unit 2^-44.  The
+// passes over the weights are chains of dependent instructions with few warps to
+// hide them, so every one counts: the integer n comes from a binary32 addition and is used
 // with its offset (which the table index and the exponent drop by themselves),
 // logits far below are raised to where the weight is 2^-64 instead of being
 // tested for, and the unit's sums keep the offset of the conversion.
